@@ -45,6 +45,8 @@
 #ifndef GQA_ATTN_H
 #define GQA_ATTN_H
 
+#include <stddef.h>
+
 #ifdef __cplusplus
 extern "C" {
 #endif
@@ -111,6 +113,101 @@ extern "C" {
 int gqa_attn_fwd(const void* q, const void* k, const void* v, void* o, int batch, int q_len,
                  int kv_len, int num_q_heads, int num_kv_heads, int head_dim, int causal,
                  int window, float softcap, void* stream);
+
+/*
+ * gqa_attn_fwd_lse -- gqa_attn_fwd that also returns every row's log-sum-exp,
+ * lse[b][h][i] = ln(sum over visible keys of e^x) in fp32 (-inf for a row
+ * without a visible key; o is zero there).  The backward pass reads it, and
+ * it merges results over disjoint sets of keys: o = sum_s e^(lse_s - lse) o_s.
+ *
+ * lse: device pointer, [batch][num_q_heads][q_len] fp32, 16-byte aligned,
+ * overlapping no other argument; the caller owns it.  Everything else,
+ * the workspace and the rules for CUDA graphs among it, is as for
+ * gqa_attn_fwd.  The kernels behind this entry point take exponentials and
+ * tanh more exactly than gqa_attn_fwd's, so o may differ from its o in the
+ * last bit.
+ */
+int gqa_attn_fwd_lse(const void* q, const void* k, const void* v, void* o, float* lse, int batch,
+                     int q_len, int kv_len, int num_q_heads, int num_kv_heads, int head_dim,
+                     int causal, int window, float softcap, void* stream);
+
+/*
+ * gqa_attn_bwd -- gradients of gqa_attn_fwd_lse's outputs with respect to q, k
+ * and v: with P = e^(x - lse) recomputed, dP = dout . v^T and
+ * delta = rowsum(dout * o) - dlse,
+ *
+ *     ds = P * (dP - delta) * (1 - tanh^2(..) with a softcap) / sqrt(head_dim)
+ *     dq = ds . k,   dk = ds^T . q,   dv = P^T . dout,
+ *
+ * dk and dv summed over the q heads of their group.  Inputs are those of the
+ * forward call, its o and lse, the gradient dout of o and, unless NULL, the
+ * gradient dlse of lse.  dout, q, o and dq are bf16 of q's shape, k, v, dk
+ * and dv bf16 of k's shape, lse and dlse fp32 [batch][num_q_heads][q_len]:
+ * dense device memory, 16-byte aligned.  P and ds are rounded to bf16 for the
+ * tensor cores, sums are fp32, each gradient is rounded once.  A row without
+ * a visible key (lse = -inf) gives and gets no gradient; a key that no query
+ * sees gets zeros.  Masked scores count as exact zeros, but a NaN or an
+ * infinity in k, v, q or dout still reaches every gradient whose products
+ * multiply it, as in a dense matrix product.
+ *
+ * scratch: caller-owned device memory, 16-byte aligned, of at least the bytes
+ * that gqa_attn_bwd_scratch reports for these sizes; its contents need not
+ * be kept or cleared.  Two calls may share it only one after the other.  The
+ * outputs and the scratch must not overlap each other or an input.
+ *
+ * The call allocates nothing and enqueues kernels (memsets when there is no
+ * query or no key) on `stream`, so it can be captured into a CUDA graph at
+ * once.  Results are deterministic.  Sizes and errors are those of
+ * gqa_attn_fwd; GQA_ATTN_ERR_ARG when the scratch is too small (see
+ * gqa_attn_last_error_detail).
+ */
+int gqa_attn_bwd(const void* dout, const void* q, const void* k, const void* v, const void* o,
+                 const float* lse, const float* dlse, void* dq, void* dk, void* dv, void* scratch,
+                 size_t scratch_bytes, int batch, int q_len, int kv_len, int num_q_heads,
+                 int num_kv_heads, int head_dim, int causal, int window, float softcap,
+                 void* stream);
+
+/* Bytes of scratch that gqa_attn_bwd needs for these sizes (host arithmetic,
+ * no device needed).  Returns GQA_ATTN_OK or gqa_attn_bwd's error for them. */
+int gqa_attn_bwd_scratch(int batch, int q_len, int kv_len, int num_q_heads, int num_kv_heads,
+                         int head_dim, int causal, int window, size_t* bytes);
+
+/* ------------------------------------------------------------------ rotary
+ * Flags of gqa_attn_rotary (bitwise or). */
+#define GQA_ROTARY_IN_SEQ_MAJOR 0x1u  /* q, k are [batch][length][heads][d]; else [batch][heads][length][d] */
+#define GQA_ROTARY_OUT_SEQ_MAJOR 0x2u /* the same for q_out, k_out */
+#define GQA_ROTARY_IN_F32 0x4u        /* q, k are fp32; else bf16 */
+#define GQA_ROTARY_OUT_F32 0x8u       /* q_out, k_out are fp32; else bf16 */
+#define GQA_ROTARY_POS_I64 0x10u      /* positions are int64; else int32 */
+#define GQA_ROTARY_INTERLEAVED 0x20u  /* pair i is elements (2i, 2i + 1); else (i, i + pairs) */
+#define GQA_ROTARY_PER_AXIS 0x40u     /* frequencies start anew on every axis */
+#define GQA_ROTARY_INVERSE 0x80u      /* turn back: the inverse, and the gradient */
+
+/*
+ * gqa_attn_rotary -- rotary positions with num_axes axes (1 to 8) on q and k.
+ *
+ * The first 2 * pairs elements of every head form pairs = sum(sections)
+ * pairs; the first sections[0] pairs belong to axis 0, the next sections[1]
+ * to axis 1, and so on.  Pair i, the j-th of its axis a, of token l of batch
+ * row b turns by positions[a][b][l] * f with f = theta^(-i / pairs), or
+ * theta^(-j / sections[a]) with GQA_ROTARY_PER_AXIS.  Elements past the last
+ * pair are copied.  Angles are exact to 1e-6 for positions of 32 bits, the
+ * rotation is fp32, rounded once.
+ *
+ * q, q_out have num_q_heads heads, k, k_out num_kv_heads; either count may be
+ * 0 (its pointers are then ignored), not both.  positions is
+ * [num_axes][batch][length] in device memory, sections host memory (read
+ * before the call returns).  head_dim % 8 == 0, 8 to 256; device pointers
+ * are 16-byte aligned.  q_out may be q (and k_out k) when type and layout do
+ * not change; nothing else may overlap an output.  Enqueues one kernel on
+ * `stream`, allocates nothing.  Errors: GQA_ATTN_ERR_ARG for unknown flags,
+ * num_axes, an empty section, too many pairs for head_dim, or a theta that is
+ * not finite and positive; the rest as for gqa_attn_fwd.
+ */
+int gqa_attn_rotary(const void* q, const void* k, void* q_out, void* k_out, const void* positions,
+                    int batch, int length, int num_q_heads, int num_kv_heads, int head_dim,
+                    int num_axes, const int* sections, double theta, unsigned int flags,
+                    void* stream);
 
 /*
  * gqa_attn_fwd_host -- the same computation for inputs and output in host

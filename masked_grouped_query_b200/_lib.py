@@ -21,6 +21,7 @@ EXPORTS = (
     "gqa_attn_version", "gqa_attn_last_error_detail", "gqa_attn_fwd_static_scratch",
     "gqa_attn_kv_append", "gqa_attn_decode_append", "gqa_attn_fwd_ring",
     "gqa_attn_describe_merge", "gqa_attn_release_workspace",
+    "gqa_attn_fwd_lse", "gqa_attn_bwd", "gqa_attn_bwd_scratch", "gqa_attn_rotary",
 )
 
 _I = ctypes.c_int
@@ -89,6 +90,15 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                                [ctypes.c_uint, _I, _I, _F, _P])
         lib.gqa_attn_fwd_ring.restype = _I
         lib.gqa_attn_fwd_ring.argtypes = ([_P] * 4 + [_I] * 7 + [ctypes.c_uint, _I, _I, _F, _P])
+        lib.gqa_attn_fwd_lse.restype = _I
+        lib.gqa_attn_fwd_lse.argtypes = [_P] * 5 + _DIMS + [_P]
+        lib.gqa_attn_bwd.restype = _I
+        lib.gqa_attn_bwd.argtypes = [_P] * 11 + [ctypes.c_size_t] + _DIMS + [_P]
+        lib.gqa_attn_bwd_scratch.restype = _I
+        lib.gqa_attn_bwd_scratch.argtypes = _DIMS[:-1] + [ctypes.POINTER(ctypes.c_size_t)]
+        lib.gqa_attn_rotary.restype = _I
+        lib.gqa_attn_rotary.argtypes = ([_P] * 5 + [_I] * 6 +
+                                        [ctypes.POINTER(_I), ctypes.c_double, ctypes.c_uint, _P])
         if path is None:
             _lib = lib
         return lib

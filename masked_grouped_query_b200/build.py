@@ -1,9 +1,11 @@
 """Build ``libgqa_attn.so`` in-tree with nvcc for sm_100a.
 
 Run ``python -m masked_grouped_query_b200.build`` (or ``__graft_entry__.build()``).
-The library is a single translation unit, ``csrc/gqa_attn.cu``, with the C ABI
-of ``include/gqa_attn.h``; it links the CUDA runtime statically and reaches
-the driver's tensor-map encoder through ``cudaGetDriverEntryPoint``.
+The library has two translation units, ``csrc/gqa_attn.cu`` (forward pass and
+KV cache) and ``csrc/gqa_train.cu`` (backward pass, rotary positions),
+compiled side by side, with the C ABI of ``include/gqa_attn.h``; it links the
+CUDA runtime statically and reaches the driver's tensor-map encoder through
+``cudaGetDriverEntryPoint``.
 """
 from __future__ import annotations
 
@@ -20,9 +22,10 @@ LIBRARY = os.path.join(PKG, "libgqa_attn.so")
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
-    "-Xcompiler", "-fPIC", "-shared",
+    "-Xcompiler", "-fPIC",
     "--expt-relaxed-constexpr",
 ]
+UNITS = ("gqa_attn", "gqa_train")
 
 
 def nvcc() -> str:
@@ -34,7 +37,7 @@ def nvcc() -> str:
 
 def sources() -> list[str]:
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC)
-                  if f.endswith((".cu", ".cuh")))
+                  if f.endswith((".cu", ".cuh", ".h")))
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -43,15 +46,29 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if (not force and os.path.exists(LIBRARY)
             and os.path.getmtime(LIBRARY) >= max(os.path.getmtime(d) for d in deps)):
         return LIBRARY
-    cmd = [nvcc(), *NVCC_FLAGS, f"-I{INCLUDE}", os.path.join(CSRC, "gqa_attn.cu"),
-           "-o", LIBRARY + ".tmp"]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + res.stderr)
-    if verbose:
-        sys.stderr.write(res.stderr)
+    # Objects carry the process number: two builds at once do not meet.
+    objects = [os.path.join(PKG, f"{u}.{os.getpid()}.o") for u in UNITS]
+    flags = [*NVCC_FLAGS, *(["-Xptxas=-v"] if verbose else []), f"-I{INCLUDE}"]
+    try:
+        compiles = [subprocess.Popen([nvcc(), *flags, "-c", os.path.join(CSRC, u + ".cu"), "-o", o],
+                                     stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+                    for u, o in zip(UNITS, objects)]
+        for u, proc in zip(UNITS, compiles):
+            out = proc.communicate()[0]
+            if proc.returncode != 0:
+                for other in compiles:
+                    other.communicate()
+                raise RuntimeError(f"nvcc failed on {u}.cu:\n{out}")
+            if verbose:
+                sys.stderr.write(out)
+        res = subprocess.run([nvcc(), *NVCC_FLAGS, "-shared", *objects, "-o", LIBRARY + ".tmp"],
+                             capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError("nvcc failed to link:\n" + res.stdout + res.stderr)
+    finally:
+        for o in objects:
+            if os.path.exists(o):
+                os.remove(o)
     os.replace(LIBRARY + ".tmp", LIBRARY)
     return LIBRARY
 

@@ -1,0 +1,345 @@
+// backward.cuh -- the backward pass of masked GQA attention: what its two
+// kernels share, and the pass over the rows that prepares their statistics.
+//
+// With s = q k^T, x = s / sqrt(D) (or cap * tanh(s / (sqrt(D) cap))) and the
+// forward's row statistics, the probabilities are recomputed,
+//   P = exp(x - lse),  0 where the mask hides the key,
+// and with dP = dO V^T and delta = rowsum(dO * O) - dlse
+//   dS = P * (dP - delta) * (1 - tanh^2 with a cap),
+//   dV = P^T dO,  dK = dS^T Q / sqrt(D),  dQ = dS K / sqrt(D).
+// The gradient of a kv head sums over the q heads of its group.
+//
+// dK and dV are sums over rows, dQ is a sum over keys.  One pass that made
+// all three would have to add dQ (or dK, dV) across CTAs; doing that in no
+// fixed order changes the result from run to run, and this library's results
+// do not change.  So two kernels each own their outputs: one walks the rows
+// of a key tile (four products: S, dP, dV, dK), the other the keys of a row
+// tile (three: S, dP, dQ).  Seven products instead of five, but no atomics,
+// no fp32 dQ buffer and no conversion pass.
+#pragma once
+
+#include "mask.cuh"
+#include "ptx.cuh"
+
+namespace gqa {
+
+constexpr float kLog2e32 = 1.4426950408889634f;
+
+// Rows as the backward kernels see them: `seqs` runs of `run` consecutive
+// rows (row r of a run is query r % q_len), cut into tiles of 128 that do not
+// cross runs.  A run is a q head when a mask makes most tiles of a head
+// skippable (q_len >= 256), else the whole group of a kv head, which wastes
+// no part of a tile at head boundaries.
+struct BwdShape {
+  int q_len, kv_len, head_dim, causal, window;
+  int run;            // rows per run
+  int runs_per_unit;  // runs of one (batch, kv head): group, or 1
+  int tiles;          // 128-row tiles per run
+  long long runs;     // batch * kv heads * runs_per_unit
+  long long units;    // batch * kv heads
+};
+
+struct BwdParams {
+  BwdShape sh;
+  const __nv_bfloat16 *q, *k, *v, *dout;
+  __nv_bfloat16 *dq, *dk, *dv;
+  const float* stats;  // [run][tile]: 128 lse (log2 units, +inf: no key), then 128 delta
+  int softcap;
+  float scale;         // 1 / sqrt(D)
+  float logit_scale;   // log2(e) / sqrt(D)
+  float cap_in;        // 1 / (sqrt(D) * cap)
+  float cap_out;       // cap * log2(e)
+};
+
+__host__ __device__ __forceinline__ MaskSpec bwd_mask(const BwdShape& s) {
+  return MaskSpec{s.q_len, s.kv_len, s.causal, s.window};
+}
+
+// The queries [lo, hi] (indexes into q_len, clamped) that see any key of
+// [k0, k1]; empty when hi < lo.
+__host__ __device__ __forceinline__ void bwd_query_range(const BwdShape& s, int k0, int k1, int& lo,
+                                                         int& hi) {
+  const long long base = (long long)s.kv_len - s.q_len;
+  long long a = 0, b = (long long)s.q_len - 1;
+  if (s.causal || s.window > 0) a = k0 - base > 0 ? k0 - base : 0;
+  if (s.window > 0) {
+    const long long e = (long long)k1 + s.window - 1 - base;
+    b = e < b ? e : b;
+  }
+  if (a > s.q_len) a = s.q_len;
+  if (b < -1) b = -1;
+  lo = (int)a;
+  hi = (int)b;
+}
+
+// Row tiles [first, first + count) of each run that a key tile has to visit.
+__host__ __device__ __forceinline__ void bwd_row_tiles(const BwdShape& s, int k0, int k1, int tile,
+                                                       int& first, int& count) {
+  int lo, hi;
+  bwd_query_range(s, k0, k1, lo, hi);
+  first = 0;
+  count = 0;
+  if (hi < lo) return;
+  if (s.run == s.q_len) {
+    first = lo / tile;
+    count = hi / tile - first + 1;
+  } else {
+    count = (s.run + tile - 1) / tile;
+  }
+}
+
+// delta and lse of every row into the tiled statistics: a group of 16
+// threads per row, 16-byte loads.  Rows that pad a run's last tile get
+// lse = +inf and delta = 0, so that their P and dS are zero.  Bound by the
+// reads of dO and O.
+__global__ void __launch_bounds__(256)
+    bwd_stats_kernel(const __nv_bfloat16* __restrict__ dout, const __nv_bfloat16* __restrict__ o,
+                     const float* __restrict__ lse, const float* __restrict__ dlse,
+                     float* __restrict__ stats, const BwdShape s) {
+  const int part = threadIdx.x & 15;
+  const long long padded = s.runs * s.tiles * 128;
+  for (long long pr = (long long)blockIdx.x * 16 + (threadIdx.x >> 4); pr < padded;
+       pr += (long long)gridDim.x * 16) {
+    const long long tile = pr >> 7;
+    const int r = (int)(pr & 127);
+    const long long run = tile / s.tiles;
+    const int in_run = (int)(tile - run * s.tiles) * 128 + r;
+    const bool live = in_run < s.run;  // the same for the row's 16 threads
+    float sum = 0.f;
+    const long long row = run * s.run + in_run;
+    if (live) {
+      const uint4* a = reinterpret_cast<const uint4*>(dout + row * s.head_dim);
+      const uint4* b = reinterpret_cast<const uint4*>(o + row * s.head_dim);
+      for (int c = part; c < s.head_dim / 8; c += 16) {
+        const uint4 x = a[c], y = b[c];
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&xs[i]));
+          const float2 g = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&ys[i]));
+          sum = fmaf(f.x, g.x, sum);
+          sum = fmaf(f.y, g.y, sum);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 8; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i, 16);
+    if (part == 0) {
+      float l2 = INFINITY;
+      if (live) {
+        const float l = lse[row];
+        l2 = l == -INFINITY ? INFINITY : l * kLog2e32;
+        if (dlse) sum -= dlse[row];
+      }
+      stats[tile * 256 + r] = l2;
+      stats[tile * 256 + 128 + r] = live ? sum : 0.f;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ mma.sync
+// The plain form of both kernels: 64 x 64 tiles on mma.sync m16n8k16.  It
+// takes every head_dim up to 256; the tcgen05 kernels take over up to 128.
+//
+// One CTA keeps the 64 rows of its own two operands in shared memory (K, V
+// for dK/dV; Q, dO for dQ) and streams 64-row tiles of the other two.  Eight
+// warps: warp w computes the 16 x 32 piece (16 own rows from w % 4, 32
+// streamed rows from w / 4) of S and dP, leaves P and dS as bf16 in shared
+// memory, and accumulates 16 own rows x half of the columns of its outputs in
+// registers (fp32).
+constexpr int kBmTile = 64;
+constexpr int kBmThreads = 256;
+
+template <int KS>
+struct BwdMmaCfg {
+  static constexpr int kPitch = KS * 16 + 8;  // elements: rows 16 bytes off a multiple of 128
+  static constexpr int kTileElems = kBmTile * kPitch;
+  static constexpr int kPPitch = kBmTile + 8;
+  static constexpr int kSmemBytes = (4 * kTileElems + 2 * kBmTile * kPPitch) * 2 + 2 * kBmTile * 4;
+};
+
+// rows [r0, r0 + n) x D of a [rows][D] matrix into a padded tile, zeros elsewhere.
+template <int KS>
+__device__ __forceinline__ void bwd_load_tile(__nv_bfloat16* dst, const __nv_bfloat16* src, int D,
+                                              int n) {
+  using C = BwdMmaCfg<KS>;
+  for (int i = threadIdx.x; i < kBmTile * KS * 2; i += kBmThreads) {
+    const int r = i / (KS * 2), c = (i - r * (KS * 2)) * 8;
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (r < n && c < D) x = *reinterpret_cast<const uint4*>(src + (long long)r * D + c);
+    *reinterpret_cast<uint4*>(dst + r * C::kPitch + c) = x;
+  }
+}
+
+template <int KS, bool kDQ>
+__global__ void __launch_bounds__(kBmThreads, 1) bwd_mma_kernel(const BwdParams p) {
+  using C = BwdMmaCfg<KS>;
+  const BwdShape& s = p.sh;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  __nv_bfloat16* own1 = (__nv_bfloat16*)smem_raw;  // K (dK/dV) or Q (dQ)
+  __nv_bfloat16* own2 = own1 + C::kTileElems;      // V or dO
+  __nv_bfloat16* str1 = own2 + C::kTileElems;      // Q or K
+  __nv_bfloat16* str2 = str1 + C::kTileElems;      // dO or V
+  __nv_bfloat16* pm = str2 + C::kTileElems;        // P  [own row][streamed row]
+  __nv_bfloat16* dm = pm + kBmTile * C::kPPitch;   // dS
+  float* st = (float*)(dm + kBmTile * C::kPPitch); // 64 lse, 64 delta of the query rows
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t4 = lane & 3, mi = lane >> 3, rr = lane & 7;
+  const int m0 = (warp & 3) * 16, half = warp >> 2, n0 = half * 32;
+  const int D = s.head_dim;
+  const MaskSpec ms = bwd_mask(s);
+
+  // Own tile, and the streamed tiles: `outer` runs of `count` tiles from `first`.
+  long long run0, unit;
+  int own_row0, own_n, first, count, outer;
+  if (kDQ) {
+    const int tiles64 = (s.run + kBmTile - 1) / kBmTile;
+    run0 = blockIdx.x / tiles64;
+    own_row0 = (int)(blockIdx.x % tiles64) * kBmTile;
+    own_n = min(kBmTile, s.run - own_row0);
+    unit = run0 / s.runs_per_unit;
+    const KeyRange kr = key_range(ms, own_row0, own_n, kBmTile);
+    first = kr.t_first;
+    count = kr.t_count;
+    outer = 1;
+    bwd_load_tile<KS>(own1, p.q + (run0 * s.run + own_row0) * D, D, own_n);
+    bwd_load_tile<KS>(own2, p.dout + (run0 * s.run + own_row0) * D, D, own_n);
+  } else {
+    const int ktiles = (s.kv_len + kBmTile - 1) / kBmTile;
+    unit = blockIdx.x / ktiles;
+    own_row0 = (int)(blockIdx.x % ktiles) * kBmTile;
+    own_n = min(kBmTile, s.kv_len - own_row0);
+    run0 = unit * s.runs_per_unit;
+    bwd_row_tiles(s, own_row0, own_row0 + own_n - 1, kBmTile, first, count);
+    outer = s.runs_per_unit;
+    bwd_load_tile<KS>(own1, p.k + (unit * s.kv_len + own_row0) * D, D, own_n);
+    bwd_load_tile<KS>(own2, p.v + (unit * s.kv_len + own_row0) * D, D, own_n);
+  }
+
+  float acc1[KS][4], acc2[kDQ ? 1 : KS][4];  // dK or dQ; dV
+#pragma unroll
+  for (int i = 0; i < KS; ++i) acc1[i][0] = acc1[i][1] = acc1[i][2] = acc1[i][3] = 0.f;
+#pragma unroll
+  for (int i = 0; i < (kDQ ? 1 : KS); ++i) acc2[i][0] = acc2[i][1] = acc2[i][2] = acc2[i][3] = 0.f;
+
+  for (int it = 0; it < outer * count; ++it) {
+    const long long run = run0 + (kDQ ? 0 : it / count);
+    const int str_row0 = (first + it % count) * kBmTile;
+    const int str_n = min(kBmTile, (kDQ ? s.kv_len : s.run) - str_row0);
+    __syncthreads();  // the previous tiles are no longer read
+    if (kDQ) {
+      bwd_load_tile<KS>(str1, p.k + (unit * s.kv_len + str_row0) * D, D, str_n);
+      bwd_load_tile<KS>(str2, p.v + (unit * s.kv_len + str_row0) * D, D, str_n);
+    } else {
+      bwd_load_tile<KS>(str1, p.q + (run * s.run + str_row0) * D, D, str_n);
+      bwd_load_tile<KS>(str2, p.dout + (run * s.run + str_row0) * D, D, str_n);
+    }
+    const int q_row0 = kDQ ? own_row0 : str_row0;
+    if (threadIdx.x < 128) {
+      const int w = threadIdx.x >> 6, r = threadIdx.x & 63;
+      st[threadIdx.x] = p.stats[(run * s.tiles + (q_row0 >> 7)) * 256 + w * 128 + (q_row0 & 127) + r];
+    }
+    __syncthreads();
+
+    // S (or S^T) and dP (or dP^T): 16 own rows x 32 streamed rows.
+    float sc[4][4], dp[4][4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sc[n][e] = dp[n][e] = 0.f;
+    {
+      const uint32_t aoff = ((m0 + (lane & 15)) * C::kPitch + (lane >> 4) * 8) * 2;
+      const uint32_t boff = ((n0 + (mi >> 1) * 8 + rr) * C::kPitch + (mi & 1) * 8) * 2;
+      const uint32_t a1 = smem_u32(own1) + aoff, a2 = smem_u32(own2) + aoff;
+      const uint32_t b1 = smem_u32(str1) + boff, b2 = smem_u32(str2) + boff;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        uint32_t x0, x1, x2, x3, y0, y1, y2, y3;
+        ldsm_x4(a1 + ks * 32, x0, x1, x2, x3);
+        ldsm_x4(a2 + ks * 32, y0, y1, y2, y3);
+#pragma unroll
+        for (int n = 0; n < 4; n += 2) {
+          uint32_t c0, c1, c2, c3;
+          ldsm_x4(b1 + n * 8 * C::kPitch * 2 + ks * 32, c0, c1, c2, c3);
+          mma_16816(sc[n], x0, x1, x2, x3, c0, c1);
+          mma_16816(sc[n + 1], x0, x1, x2, x3, c2, c3);
+          ldsm_x4(b2 + n * 8 * C::kPitch * 2 + ks * 32, c0, c1, c2, c3);
+          mma_16816(dp[n], y0, y1, y2, y3, c0, c1);
+          mma_16816(dp[n + 1], y0, y1, y2, y3, c2, c3);
+        }
+      }
+    }
+    // P and dS, rounded to bf16 for the tensor cores as the forward's P is.
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int own = m0 + g + 8 * h, col = n0 + n * 8 + 2 * t4;
+        float pv[2], dv[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int qr = kDQ ? own : col + e, kr = kDQ ? col + e : own;
+          const int key = (kDQ ? str_row0 : own_row0) + kr;
+          const int qpos = s.kv_len - s.q_len + (q_row0 + qr) % s.q_len;
+          const bool see = key >= first_key(ms, qpos) && key <= last_key(ms, qpos);
+          const float x = sc[n][2 * h + e];
+          float t = 0.f, y;
+          if (p.softcap) {
+            t = tanh_accurate(x * p.cap_in);
+            y = p.cap_out * t;
+          } else {
+            y = x * p.logit_scale;
+          }
+          const float pr = see ? ex2(y - st[qr]) : 0.f;
+          const float d = pr * (dp[n][2 * h + e] - st[64 + qr]) * (1.f - t * t);
+          pv[e] = pr;
+          dv[e] = see ? d : 0.f;
+        }
+        if (!kDQ) *(uint32_t*)(pm + own * C::kPPitch + col) = pack_bf16(pv[0], pv[1]);
+        *(uint32_t*)(dm + own * C::kPPitch + col) = pack_bf16(dv[0], dv[1]);
+      }
+    __syncthreads();
+    // Outputs: 16 own rows x half of the columns, over the 64 streamed rows.
+    {
+      const uint32_t aoff = ((m0 + (lane & 15)) * C::kPPitch + (lane >> 4) * 8) * 2;
+      const uint32_t ad = smem_u32(dm) + aoff, ap = smem_u32(pm) + aoff;
+      const uint32_t boff = (((mi & 1) * 8 + rr) * C::kPitch + half * KS * 8 + (mi >> 1) * 8) * 2;
+      const uint32_t b1 = smem_u32(str1) + boff, b2 = smem_u32(str2) + boff;
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        uint32_t x0, x1, x2, x3, y0 = 0, y1 = 0, y2 = 0, y3 = 0;
+        ldsm_x4(ad + ks * 32, x0, x1, x2, x3);
+        if (!kDQ) ldsm_x4(ap + ks * 32, y0, y1, y2, y3);
+#pragma unroll
+        for (int n = 0; n < KS; n += 2) {
+          uint32_t c0, c1, c2, c3;
+          ldsm_x4_t(b1 + (ks * 16 * C::kPitch + n * 8) * 2, c0, c1, c2, c3);
+          mma_16816(acc1[n], x0, x1, x2, x3, c0, c1);
+          mma_16816(acc1[n + 1], x0, x1, x2, x3, c2, c3);
+          if constexpr (!kDQ) {
+            ldsm_x4_t(b2 + (ks * 16 * C::kPitch + n * 8) * 2, c0, c1, c2, c3);
+            mma_16816(acc2[n], y0, y1, y2, y3, c0, c1);
+            mma_16816(acc2[n + 1], y0, y1, y2, y3, c2, c3);
+          }
+        }
+      }
+    }
+  }
+
+  const long long out0 = kDQ ? run0 * s.run + own_row0 : unit * s.kv_len + own_row0;
+#pragma unroll
+  for (int n = 0; n < KS; ++n)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = m0 + g + 8 * h, c = half * KS * 8 + n * 8 + 2 * t4;
+      if (r >= own_n || c >= D) continue;
+      const long long off = (out0 + r) * D + c;
+      *(uint32_t*)((kDQ ? p.dq : p.dk) + off) =
+          pack_bf16(acc1[n][2 * h] * p.scale, acc1[n][2 * h + 1] * p.scale);
+      if constexpr (!kDQ)
+        *(uint32_t*)(p.dv + off) = pack_bf16(acc2[n][2 * h], acc2[n][2 * h + 1]);
+    }
+}
+
+}  // namespace gqa

@@ -59,6 +59,7 @@ struct DecodeParams {
   float* part_o;       // [unit][rb][split][block_rows][head_dim]  (o_s, normalised)
   float* part_lse;     // [unit][rb][split][block_rows]            (log2 domain)
   unsigned int* tickets;  // [unit][rb], zero between calls
+  float* lse;             // kLse kernels: log-sum-exp per row, natural logarithm
 };
 
 // kDeep: a 5-stage ring (160 KB in flight for KS = 8) for grids of at most
@@ -83,7 +84,10 @@ struct DecodeCfg {
 // rows), with P^T moved into the B-operand layout by movmatrix -- so the
 // padded rows cost half as much as in the rows-as-M form and the O
 // accumulator needs half the registers (two CTAs per SM).
-template <int KS, bool kT, bool kDeep = false>
+//
+// kLse: also returns every row's log-sum-exp in fp32, with an accurate tanh
+// in place of the hardware's (5e-4 relative).
+template <int KS, bool kT, bool kDeep = false, bool kLse = false>
 __global__ void __maxnreg__(kT ? 128 : 255)
     decode_splitkv_kernel(const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v, const DecodeParams p) {
@@ -259,6 +263,7 @@ __global__ void __maxnreg__(kT ? 128 : 255)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float v = !p.use_softcap ? sc[e] * p.logit_scale
+                  : kLse         ? p.cap_out * tanh_accurate(sc[e] * p.cap_in)
                   : small        ? p.cap_out * tanh_poly_small(sc[e] * p.cap_in)
                                  : p.cap_out * tanh_fast(sc[e] * p.cap_in);
         if (need_mask) {
@@ -402,7 +407,12 @@ __global__ void __maxnreg__(kT ? 128 : 255)
       // ---- logits (log2 domain), softcap, mask.  With a softcap the tanh is
       // an FMA-pipe polynomial when every |x / s| of the warp is <= 1/2.
       float x[2][4];
-      if (p.use_softcap) {
+      if (kLse && p.use_softcap) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[n][e] = p.cap_out * tanh_accurate(sc[n][e] * p.cap_in);
+      } else if (p.use_softcap) {
         float am = 0.f;
 #pragma unroll
         for (int n = 0; n < 2; ++n)
@@ -536,6 +546,9 @@ __global__ void __maxnreg__(kT ? 128 : 255)
     const float o_val = L > 0.f ? O / L : 0.f;
     if (direct) {
       p.o[((long long)unit * p.rows + r0 + row) * D + d] = __float2bfloat16_rn(o_val);
+      if (kLse && d == 0)
+        p.lse[(long long)unit * p.rows + r0 + row] =
+            L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
     } else {
       p.part_o[(prow0 + row) * D + d] = o_val;
       if (d == 0) p.part_lse[prow0 + row] = L > 0.f ? M + log2f(L) : -INFINITY;
@@ -572,6 +585,9 @@ __global__ void __maxnreg__(kT ? 128 : 255)
       L += f;
     }
     const float inv = L > 0.f ? 1.0f / L : 0.f;
+    if (kLse)
+      p.lse[(long long)unit * p.rows + r0 + row] =
+          L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
     for (int s = 0; s < p.splits; ++s) wgt[s * nr + row] *= inv;
   }
   asm volatile("bar.sync 1, %0;" ::"r"(kDecComputeWarps * 32) : "memory");

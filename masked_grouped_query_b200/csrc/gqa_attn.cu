@@ -1,13 +1,17 @@
-// gqa_attn.cu -- host side of libgqa_attn.so: argument validation, planning,
-// tensor maps, workspace and launches behind the C ABI of gqa_attn.h.
+// gqa_attn.cu -- host side of the forward pass and the KV cache in
+// libgqa_attn.so: argument validation, planning, tensor maps, workspace and
+// launches behind the C ABI of gqa_attn.h.
 //
-// Single translation unit: the kernels are included below.
+// The kernels are included below.  gqa_train.cu, the library's other
+// translation unit, holds the backward pass and the rotary positions; it
+// reaches the shared host pieces through host.h.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
 #include <atomic>
 #include <cmath>
+#include <cstdarg>
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
@@ -17,6 +21,7 @@
 #include <vector>
 
 #include "gqa_attn.h"
+#include "host.h"
 #include "status.cuh"
 #include "ptx.cuh"
 #include "mask.cuh"
@@ -36,8 +41,8 @@ struct DeviceInfo {
   bool probed = false;
   int sms = 0, major = 0, minor = 0;
   int smem_optin = 0;
-  bool decode_attr[10] = {};  // per instantiation: [0, 8) 3/2-stage, [8, 10) 5-stage
-  bool prefill_attr[24] = {};  // per (DCH, softcap code, split mode) instantiation
+  bool decode_attr[20] = {};  // per instantiation: [0, 8) 3/2-stage, [8, 10) 5-stage; + 10 with lse
+  bool prefill_attr[32] = {};  // per (DCH, softcap code, split mode) instantiation; [24, 32) with lse
   int append_blocks[4] = {};    // resident kv_append blocks per SM, per instantiation
   bool append_runs_ready[4] = {};  // staged-runs kernel's smem attribute set
   // Clusters of n CTAs of a split instantiation that can be resident at once
@@ -100,6 +105,7 @@ struct Problem {
   int app_count = 0, app_pos = 0, app_new_f32 = 0, app_new_head_major = 0;
   const void* app_new_k = nullptr;
   const void* app_new_v = nullptr;
+  float* lse = nullptr;  // row statistics wanted ([batch][hq][q_len]); runs the kLse kernels
 };
 
 int validate(int batch, int q_len, int kv_len, int hq, int hkv, int d, int causal, int window,
@@ -417,19 +423,19 @@ int encode_map(CUtensorMap* map, const void* base, int cols, long long rows, lon
 }
 
 // ------------------------------------------------------------------ launches
-template <int KS, bool kT, bool kDeep = false>
+template <int KS, bool kT, bool kDeep, bool kLse>
 int launch_decode_ks(const Problem& pr, const Plan& pl, DeviceInfo& dev, const void* q,
                      const void* k, const void* v, void* o, void* ws, void* tickets,
                      cudaStream_t stream) {
   using C = DecodeCfg<KS, kDeep>;
-  const int slot = kDeep ? 8 + (KS / 4 - 1) : (KS / 4 - 1) + (kT ? 4 : 0);
+  const int slot = (kDeep ? 8 + (KS / 4 - 1) : (KS / 4 - 1) + (kT ? 4 : 0)) + (kLse ? 10 : 0);
   std::unique_lock<std::mutex> lk(g_mu);
   if (!dev.decode_attr[slot]) {
-    cudaError_t e = cudaFuncSetAttribute(decode_splitkv_kernel<KS, kT, kDeep>,
+    cudaError_t e = cudaFuncSetAttribute(decode_splitkv_kernel<KS, kT, kDeep, kLse>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          C::kSmemBytes);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(decode_splitkv_kernel<KS, kT, kDeep>,
+      e = cudaFuncSetAttribute(decode_splitkv_kernel<KS, kT, kDeep, kLse>,
                                cudaFuncAttributePreferredSharedMemoryCarveout,
                                cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute(decode)", e, GQA_ATTN_ERR_LAUNCH);
@@ -476,13 +482,15 @@ int launch_decode_ks(const Problem& pr, const Plan& pl, DeviceInfo& dev, const v
   p.part_o = (float*)ws;
   p.part_lse = ws ? (float*)((char*)ws + pl.off_lse) : nullptr;
   p.tickets = (unsigned int*)tickets;
-  decode_splitkv_kernel<KS, kT, kDeep>
+  p.lse = pr.lse;
+  decode_splitkv_kernel<KS, kT, kDeep, kLse>
       <<<dim3((unsigned)pl.ctas), kDecThreads, C::kSmemBytes, stream>>>(tk, tv, p);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? GQA_ATTN_OK : cuda_fail("launch(decode)", e, GQA_ATTN_ERR_LAUNCH);
 }
 
-int launch_decode(const Problem& pr, const Plan& pl, DeviceInfo& dev, const void* q,
+template <bool kLse>
+int launch_decode_lse(const Problem& pr, const Plan& pl, DeviceInfo& dev, const void* q,
                   const void* k, const void* v, void* o, void* ws, void* tickets,
                   cudaStream_t stream) {
   if (pl.block_rows <= 8) {  // single-token decode shapes: keys-as-M variant
@@ -490,21 +498,28 @@ int launch_decode(const Problem& pr, const Plan& pl, DeviceInfo& dev, const void
     const bool deep = pl.ctas <= dev.sms;
     switch (pl.ks) {
       case 4:
-        return deep ? launch_decode_ks<4, true, true>(pr, pl, dev, q, k, v, o, ws, tickets, stream)
-                    : launch_decode_ks<4, true>(pr, pl, dev, q, k, v, o, ws, tickets, stream);
+        return deep ? launch_decode_ks<4, true, true, kLse>(pr, pl, dev, q, k, v, o, ws, tickets, stream)
+                    : launch_decode_ks<4, true, false, kLse>(pr, pl, dev, q, k, v, o, ws, tickets, stream);
       case 8:
-        return deep ? launch_decode_ks<8, true, true>(pr, pl, dev, q, k, v, o, ws, tickets, stream)
-                    : launch_decode_ks<8, true>(pr, pl, dev, q, k, v, o, ws, tickets, stream);
-      case 12: return launch_decode_ks<12, true>(pr, pl, dev, q, k, v, o, ws, tickets, stream);
-      default: return launch_decode_ks<16, true>(pr, pl, dev, q, k, v, o, ws, tickets, stream);
+        return deep ? launch_decode_ks<8, true, true, kLse>(pr, pl, dev, q, k, v, o, ws, tickets, stream)
+                    : launch_decode_ks<8, true, false, kLse>(pr, pl, dev, q, k, v, o, ws, tickets, stream);
+      case 12: return launch_decode_ks<12, true, false, kLse>(pr, pl, dev, q, k, v, o, ws, tickets, stream);
+      default: return launch_decode_ks<16, true, false, kLse>(pr, pl, dev, q, k, v, o, ws, tickets, stream);
     }
   }
   switch (pl.ks) {
-    case 4: return launch_decode_ks<4, false>(pr, pl, dev, q, k, v, o, ws, tickets, stream);
-    case 8: return launch_decode_ks<8, false>(pr, pl, dev, q, k, v, o, ws, tickets, stream);
-    case 12: return launch_decode_ks<12, false>(pr, pl, dev, q, k, v, o, ws, tickets, stream);
-    default: return launch_decode_ks<16, false>(pr, pl, dev, q, k, v, o, ws, tickets, stream);
+    case 4: return launch_decode_ks<4, false, false, kLse>(pr, pl, dev, q, k, v, o, ws, tickets, stream);
+    case 8: return launch_decode_ks<8, false, false, kLse>(pr, pl, dev, q, k, v, o, ws, tickets, stream);
+    case 12: return launch_decode_ks<12, false, false, kLse>(pr, pl, dev, q, k, v, o, ws, tickets, stream);
+    default: return launch_decode_ks<16, false, false, kLse>(pr, pl, dev, q, k, v, o, ws, tickets, stream);
   }
+}
+
+int launch_decode(const Problem& pr, const Plan& pl, DeviceInfo& dev, const void* q,
+                  const void* k, const void* v, void* o, void* ws, void* tickets,
+                  cudaStream_t stream) {
+  return pr.lse ? launch_decode_lse<true>(pr, pl, dev, q, k, v, o, ws, tickets, stream)
+                : launch_decode_lse<false>(pr, pl, dev, q, k, v, o, ws, tickets, stream);
 }
 
 // Exponent-base offset B of the fixed-base softcap path for this cap (in
@@ -516,8 +531,10 @@ float cap_base_offset(float cap_out) { return std::max(16.0f, 2.0f * cap_out - 1
 // tanh polynomial with a fixed exponent base (no row max; caps up to about
 // 63.8); 5 = the degree-5 polynomial with the row max (caps up to
 // kTanh5MaxCap, or any cap when override key 5 asks for it); 7 = degree 7.
+// With row statistics wanted: always 7 (the kLse kernels put degree 9 there).
 int cap_degree(const Problem& pr) {
   if (!(pr.softcap > 0.f)) return 0;
+  if (pr.lse) return 7;
   if (pr.softcap > kTanh5MaxCap) return 7;
   const bool fixed = cap_base_offset(pr.softcap * kLog2e) <= 64.0f && g_force_two_pass.load() == 0;
   return fixed ? 3 : 5;
@@ -525,31 +542,32 @@ int cap_degree(const Problem& pr) {
 
 // kSplit: 0 = no key splits, 1 = splits merged through the workspace,
 // 2 = paired splits merged inside a cluster.
-template <int DCH, int kCapDeg, int kSplit>
+template <int DCH, int kCapDeg, int kSplit, bool kLse = false>
 constexpr int prefill_slot() {
+  if (kLse) return 24 + (DCH - 1) + 2 * (kCapDeg == 7 ? 1 : 0) + 4 * kSplit;
   return (DCH - 1) + 2 * (kCapDeg == 5 ? 1 : kCapDeg == 7 ? 2 : kCapDeg == 3 ? 3 : 0) +
          8 * kSplit;
 }
 
 // One-time per device and instantiation (under g_mu): the register-split
 // check and the dynamic shared memory limit.
-template <int DCH, int kCapDeg, int kSplit>
+template <int DCH, int kCapDeg, int kSplit, bool kLse = false>
 int prefill_setup(DeviceInfo& dev) {
   using C = PrefillCfg<DCH>;
-  constexpr int attr = prefill_slot<DCH, kCapDeg, kSplit>();
+  constexpr int attr = prefill_slot<DCH, kCapDeg, kSplit, kLse>();
   std::lock_guard<std::mutex> lk(g_mu);
   if (dev.prefill_attr[attr]) return GQA_ATTN_OK;
   // The register split inside the kernel must fit what the block is
   // launched with, or setmaxnreg.inc could never be granted.
   cudaFuncAttributes fa;
-  const cudaError_t ea = cudaFuncGetAttributes(&fa, prefill_sm100_kernel<DCH, kCapDeg, kSplit>);
+  const cudaError_t ea = cudaFuncGetAttributes(&fa, prefill_sm100_kernel<DCH, kCapDeg, kSplit, kLse>);
   if (ea != cudaSuccess) return cuda_fail("cudaFuncGetAttributes(prefill)", ea, GQA_ATTN_ERR_LAUNCH);
   if ((long long)fa.numRegs * kPfThreads < kRegSplitTotal) {
     snprintf(g_detail, sizeof g_detail, "prefill kernel built with %d registers/thread: "
              "register split needs %d", fa.numRegs, kRegSplitTotal);
     return GQA_ATTN_ERR_LAUNCH;
   }
-  const cudaError_t e = cudaFuncSetAttribute(prefill_sm100_kernel<DCH, kCapDeg, kSplit>,
+  const cudaError_t e = cudaFuncSetAttribute(prefill_sm100_kernel<DCH, kCapDeg, kSplit, kLse>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              C::kSmemBytes);
   if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute(prefill)", e, GQA_ATTN_ERR_LAUNCH);
@@ -611,13 +629,13 @@ int prefill_cluster(const Problem& pr, const Plan& pl, DeviceInfo& dev, int* csi
                   : prefill_cluster_k<2, 0>(pr, pl, dev, csize);
 }
 
-template <int DCH, int kCapDeg, int kSplit>
+template <int DCH, int kCapDeg, int kSplit, bool kLse = false>
 int launch_prefill_k(const Problem& pr, const Plan& pl, DeviceInfo& dev, int csize,
                      const void* q, const void* k, const void* v, void* o, void* ws,
                      void* tickets, cudaStream_t stream) {
   using C = PrefillCfg<DCH>;
   constexpr bool kCap = kCapDeg != 0;
-  int rc = prefill_setup<DCH, kCapDeg, kSplit>(dev);
+  int rc = prefill_setup<DCH, kCapDeg, kSplit, kLse>(dev);
   if (rc != GQA_ATTN_OK) return rc;
   CUtensorMap tq, tk, tv, to;
   if (encode_map(&tq, q, pr.d, pr.rows, pr.units, kPfM) != GQA_ATTN_OK ||
@@ -641,6 +659,7 @@ int launch_prefill_k(const Problem& pr, const Plan& pl, DeviceInfo& dev, int csi
   p.ws_o = (float*)ws;
   p.ws_ml = ws ? (float*)((char*)ws + pl.off_lse) : nullptr;
   p.tickets = (unsigned int*)tickets;
+  p.lse = pr.lse;
   p.pair_heads = pl.pair_heads;
   p.heavy_first = (pr.causal || pr.window > 0) && !pl.split_pairs ? 1 : 0;
   p.cluster_merge = kSplit == 2 ? csize : 0;
@@ -673,8 +692,8 @@ int launch_prefill_k(const Problem& pr, const Plan& pl, DeviceInfo& dev, int csi
   }
   // Persistent: at most one CTA per SM, each walking items with stride grid.
   const int grid = (int)(pl.ctas < dev.sms ? pl.ctas : dev.sms);
-  prefill_sm100_kernel<DCH, kCapDeg, kSplit><<<dim3((unsigned)grid), kPfThreads, C::kSmemBytes, stream>>>(
-      tq, tk, tv, to, p);
+  prefill_sm100_kernel<DCH, kCapDeg, kSplit, kLse>
+      <<<dim3((unsigned)grid), kPfThreads, C::kSmemBytes, stream>>>(tq, tk, tv, to, p);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? GQA_ATTN_OK : cuda_fail("launch(prefill)", e, GQA_ATTN_ERR_LAUNCH);
 }
@@ -694,6 +713,15 @@ int launch_prefill(const Problem& pr, const Plan& pl, DeviceInfo& dev, int csize
                    const void* k, const void* v, void* o, void* ws, void* tickets,
                    cudaStream_t stream) {
   const int deg = cap_degree(pr);
+  if (pr.lse) {  // splits merge by ticket (csize is 0)
+    auto go = [&](auto fn) { return fn(pr, pl, dev, 0, q, k, v, o, ws, tickets, stream); };
+    const bool split = pl.splits > 1;
+    if (pl.dch == 1)
+      return deg ? go(split ? launch_prefill_k<1, 7, 1, true> : launch_prefill_k<1, 7, 0, true>)
+                 : go(split ? launch_prefill_k<1, 0, 1, true> : launch_prefill_k<1, 0, 0, true>);
+    return deg ? go(split ? launch_prefill_k<2, 7, 1, true> : launch_prefill_k<2, 7, 0, true>)
+               : go(split ? launch_prefill_k<2, 0, 1, true> : launch_prefill_k<2, 0, 0, true>);
+  }
   if (pl.dch == 1)
     return deg == 3 ? launch_prefill_d<1, 3>(pr, pl, dev, csize, q, k, v, o, ws, tickets, stream)
          : deg == 5 ? launch_prefill_d<1, 5>(pr, pl, dev, csize, q, k, v, o, ws, tickets, stream)
@@ -746,6 +774,12 @@ int check_pointers(const Problem& pr, const void* q, const void* k, const void* 
   return GQA_ATTN_OK;
 }
 
+__global__ void fill_kernel(float* x, long long n, float value) {
+  for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < n;
+       i += (long long)gridDim.x * blockDim.x)
+    x[i] = value;
+}
+
 int run(const Problem& pr, const void* q, const void* k, const void* v, void* o,
         cudaStream_t stream) {
   DeviceInfo* dev = nullptr;
@@ -759,14 +793,19 @@ int run(const Problem& pr, const void* q, const void* k, const void* v, void* o,
       return GQA_ATTN_OK;
     case kPathZero: {
       const size_t bytes = (size_t)pr.batch * pr.hq * (size_t)pr.q_len * pr.d * 2;
-      return cudaMemsetAsync(o, 0, bytes, stream) == cudaSuccess ? GQA_ATTN_OK
-                                                                 : GQA_ATTN_ERR_LAUNCH;
+      if (cudaMemsetAsync(o, 0, bytes, stream) != cudaSuccess) return GQA_ATTN_ERR_LAUNCH;
+      if (!pr.lse) return GQA_ATTN_OK;
+      const long long n = (long long)pr.batch * pr.hq * pr.q_len;
+      const long long blocks = ceil_div(n, 256);
+      fill_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, stream>>>(pr.lse, n, -INFINITY);
+      const cudaError_t e = cudaGetLastError();
+      return e == cudaSuccess ? GQA_ATTN_OK : cuda_fail("launch(fill)", e, GQA_ATTN_ERR_LAUNCH);
     }
     default: {
       // Key splits merge through the workspace: by the last CTA of a unit to
       // finish (ticket), or by all CTAs of the unit's cluster together.
       int csize = 0;
-      if (pl.path == kPathPrefill && pl.splits > 1) {
+      if (pl.path == kPathPrefill && pl.splits > 1 && !pr.lse) {
         rc = prefill_cluster(pr, pl, *dev, &csize);
         if (rc != GQA_ATTN_OK) return rc;
       }
@@ -815,6 +854,35 @@ int static_scratch(void** out) {
 
 }  // namespace
 
+namespace gqa_host {
+
+int device(int* index, int* sms) {
+  DeviceInfo* dev = nullptr;
+  const int rc = device_info(&dev);
+  if (rc != GQA_ATTN_OK) return rc;
+  *index = (int)(dev - g_dev);
+  *sms = dev->sms;
+  return GQA_ATTN_OK;
+}
+int tensor_map(CUtensorMap* map, const void* base, int cols, long long rows, long long outer,
+               int box_rows) {
+  return encode_map(map, base, cols, rows, outer, box_rows);
+}
+int forced_path() { return g_force_path.load(); }
+int cuda_fail(const char* where, cudaError_t e, int code) { return ::cuda_fail(where, e, code); }
+int detail(int code, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_detail, sizeof g_detail, fmt, ap);
+  va_end(ap);
+  return code;
+}
+bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
+  return ::overlaps(a, na, b, nb);
+}
+
+}  // namespace gqa_host
+
 // ==================================================================== C ABI
 extern "C" {
 
@@ -827,6 +895,28 @@ int gqa_attn_fwd(const void* q, const void* k, const void* v, void* o, int batch
   if (rc != GQA_ATTN_OK) return rc;
   rc = check_pointers(pr, q, k, v, o);
   if (rc != GQA_ATTN_OK) return rc;
+  return run(pr, q, k, v, o, (cudaStream_t)stream);
+}
+
+int gqa_attn_fwd_lse(const void* q, const void* k, const void* v, void* o, float* lse, int batch,
+                     int q_len, int kv_len, int num_q_heads, int num_kv_heads, int head_dim,
+                     int causal, int window, float softcap, void* stream) {
+  Problem pr;
+  int rc = validate(batch, q_len, kv_len, num_q_heads, num_kv_heads, head_dim, causal, window,
+                    softcap, &pr);
+  if (rc != GQA_ATTN_OK) return rc;
+  rc = check_pointers(pr, q, k, v, o);
+  if (rc != GQA_ATTN_OK) return rc;
+  const size_t rows = (size_t)batch * num_q_heads * (size_t)q_len;
+  const size_t q_bytes = rows * head_dim * 2, lse_bytes = rows * 4;
+  const size_t kv_bytes = (size_t)batch * num_kv_heads * (size_t)kv_len * head_dim * 2;
+  if (rows && !lse) return GQA_ATTN_ERR_NULL_POINTER;
+  if ((uintptr_t)lse & 15u) return GQA_ATTN_ERR_MISALIGNED;
+  if (overlaps(lse, lse_bytes, o, q_bytes) || overlaps(lse, lse_bytes, q, q_bytes) ||
+      overlaps(lse, lse_bytes, k, kv_bytes) || overlaps(lse, lse_bytes, v, kv_bytes))
+    return GQA_ATTN_ERR_ALIAS;
+  if (rows == 0) return GQA_ATTN_OK;
+  pr.lse = lse;
   return run(pr, q, k, v, o, (cudaStream_t)stream);
 }
 
@@ -924,12 +1014,16 @@ const char* gqa_attn_error_string(int status) {
 int gqa_attn_status(void) {
   uint32_t v = 0;
   if (cudaMemcpyFromSymbol(&v, gqa::g_gqa_status, sizeof v) != cudaSuccess) return -1;
-  return (int)v;
+  uint32_t w = 0;
+  if (gqa_host::train_status(&w) != cudaSuccess) return -1;
+  return (int)(v | w);
 }
 
 int gqa_attn_clear_status(void) {
   const uint32_t z = 0;
-  if (cudaMemcpyToSymbol(gqa::g_gqa_status, &z, sizeof z) != cudaSuccess) return GQA_ATTN_ERR_LAUNCH;
+  if (cudaMemcpyToSymbol(gqa::g_gqa_status, &z, sizeof z) != cudaSuccess ||
+      gqa_host::train_clear_status() != cudaSuccess)
+    return GQA_ATTN_ERR_LAUNCH;
   // A kernel that gave up a wait may have left split tickets counted, which
   // would make the next merge on that buffer start early or never: zero
   // every ticket buffer of this device (active and retired).

@@ -1,0 +1,313 @@
+// gqa_train.cu -- host side of the backward pass and of the rotary positions
+// in libgqa_attn.so: argument checks, plans and launches behind the C ABI of
+// gqa_attn.h.  The kernels are included below; gqa_attn.cu holds the rest of
+// the library.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "gqa_attn.h"
+#include "host.h"
+#include "status.cuh"
+#include "ptx.cuh"
+#include "mask.cuh"
+#include "backward.cuh"
+#include "rotary.cuh"
+
+namespace {
+
+using namespace gqa;
+using gqa_host::cuda_fail;
+using gqa_host::detail;
+using gqa_host::overlaps;
+
+std::mutex g_attr_mu;
+constexpr int kMaxDevices = 64;
+
+inline long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+// Sets a kernel's dynamic shared memory limit once per device.
+template <typename K>
+int allow_smem(K kernel, int bytes, int device, bool* done) {
+  std::lock_guard<std::mutex> lk(g_attr_mu);
+  if (done[device]) return GQA_ATTN_OK;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute(backward)", e, GQA_ATTN_ERR_LAUNCH);
+  done[device] = true;
+  return GQA_ATTN_OK;
+}
+
+int launched(const char* where) {
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? GQA_ATTN_OK : cuda_fail(where, e, GQA_ATTN_ERR_LAUNCH);
+}
+
+// ------------------------------------------------------------------ backward
+// Sizes and the row layout of a backward call (see BwdShape).
+int bwd_shape(int batch, int q_len, int kv_len, int hq, int hkv, int d, int causal, int window,
+              BwdShape* s) {
+  if (batch < 0 || q_len < 0 || kv_len < 0 || hq < 1 || hkv < 1) return GQA_ATTN_ERR_BAD_SHAPE;
+  if (hq % hkv != 0) return GQA_ATTN_ERR_HEAD_RATIO;
+  if (d < 8 || d > 256 || d % 8 != 0) return GQA_ATTN_ERR_HEAD_DIM;
+  const int group = hq / hkv;
+  // Row and key indexes are 32-bit, with room for the last tile's padding.
+  constexpr long long kMost = 0x7fffff00LL;
+  if ((long long)group * q_len > kMost || kv_len > kMost || (long long)batch * hq > kMost)
+    return GQA_ATTN_ERR_TOO_LARGE;
+  s->q_len = q_len;
+  s->kv_len = kv_len;
+  s->head_dim = d;
+  s->causal = causal ? 1 : 0;
+  s->window = window > 0 ? window : 0;
+  const bool per_head = (s->causal || s->window) && q_len >= 256;
+  s->runs_per_unit = per_head ? group : 1;
+  s->run = per_head ? q_len : group * q_len;
+  s->tiles = (int)ceil_div(s->run, 128);
+  s->units = (long long)batch * hkv;
+  s->runs = s->units * s->runs_per_unit;
+  // One block per row tile and per key tile (64 rows at the least), and the
+  // statistics' bytes in a size_t with room to spare.
+  if (s->runs * s->tiles * 2 > kMost || s->units * ceil_div(kv_len, 64) > kMost)
+    return GQA_ATTN_ERR_TOO_LARGE;
+  return GQA_ATTN_OK;
+}
+
+size_t bwd_scratch_bytes(const BwdShape& s) {
+  return (size_t)s.runs * (size_t)s.tiles * 256 * sizeof(float);
+}
+
+template <int KS>
+int launch_bwd_mma(const BwdParams& p, int device, cudaStream_t st) {
+  using C = BwdMmaCfg<KS>;
+  static bool done_kv[kMaxDevices], done_q[kMaxDevices];
+  int rc = allow_smem(bwd_mma_kernel<KS, false>, C::kSmemBytes, device, done_kv);
+  if (rc == GQA_ATTN_OK) rc = allow_smem(bwd_mma_kernel<KS, true>, C::kSmemBytes, device, done_q);
+  if (rc != GQA_ATTN_OK) return rc;
+  const long long key_tiles = p.sh.units * ceil_div(p.sh.kv_len, kBmTile);
+  bwd_mma_kernel<KS, false><<<(unsigned)key_tiles, kBmThreads, C::kSmemBytes, st>>>(p);
+  if ((rc = launched("launch(backward dK dV)")) != GQA_ATTN_OK) return rc;
+  const long long row_tiles = p.sh.runs * ceil_div(p.sh.run, kBmTile);
+  bwd_mma_kernel<KS, true><<<(unsigned)row_tiles, kBmThreads, C::kSmemBytes, st>>>(p);
+  return launched("launch(backward dQ)");
+}
+
+// ------------------------------------------------------------------ rotary
+template <int V, typename TI, typename TO>
+int launch_rotary(const RotaryParams& p, bool interleaved, dim3 grid, cudaStream_t st) {
+  if (interleaved)
+    rotary_kernel<V, TI, TO, true><<<grid, kRotThreads, 0, st>>>(p);
+  else
+    rotary_kernel<V, TI, TO, false><<<grid, kRotThreads, 0, st>>>(p);
+  return launched("launch(rotary)");
+}
+
+template <int V>
+int launch_rotary_types(const RotaryParams& p, bool in32, bool out32, bool interleaved, dim3 grid,
+                        cudaStream_t st) {
+  using B = __nv_bfloat16;
+  if (in32)
+    return out32 ? launch_rotary<V, float, float>(p, interleaved, grid, st)
+                 : launch_rotary<V, float, B>(p, interleaved, grid, st);
+  return out32 ? launch_rotary<V, B, float>(p, interleaved, grid, st)
+               : launch_rotary<V, B, B>(p, interleaved, grid, st);
+}
+
+}  // namespace
+
+namespace gqa_host {
+
+cudaError_t train_status(uint32_t* word) {
+  return cudaMemcpyFromSymbol(word, gqa::g_gqa_status, sizeof *word);
+}
+cudaError_t train_clear_status() {
+  const uint32_t z = 0;
+  return cudaMemcpyToSymbol(gqa::g_gqa_status, &z, sizeof z);
+}
+
+}  // namespace gqa_host
+
+extern "C" {
+
+int gqa_attn_bwd_scratch(int batch, int q_len, int kv_len, int num_q_heads, int num_kv_heads,
+                         int head_dim, int causal, int window, size_t* bytes) {
+  BwdShape s;
+  const int rc = bwd_shape(batch, q_len, kv_len, num_q_heads, num_kv_heads, head_dim, causal,
+                           window, &s);
+  if (rc != GQA_ATTN_OK) return rc;
+  if (bytes) *bytes = bwd_scratch_bytes(s);
+  return GQA_ATTN_OK;
+}
+
+int gqa_attn_bwd(const void* dout, const void* q, const void* k, const void* v, const void* o,
+                 const float* lse, const float* dlse, void* dq, void* dk, void* dv, void* scratch,
+                 size_t scratch_bytes, int batch, int q_len, int kv_len, int num_q_heads,
+                 int num_kv_heads, int head_dim, int causal, int window, float softcap,
+                 void* stream) {
+  BwdParams p;
+  BwdShape& s = p.sh;
+  int rc = bwd_shape(batch, q_len, kv_len, num_q_heads, num_kv_heads, head_dim, causal, window, &s);
+  if (rc != GQA_ATTN_OK) return rc;
+  if (!(softcap >= 0.0f) || std::isinf(softcap)) return GQA_ATTN_ERR_SOFTCAP;
+  const size_t rows = (size_t)batch * num_q_heads * (size_t)q_len;
+  const size_t q_bytes = rows * head_dim * 2, stat_bytes = rows * 4;
+  const size_t kv_bytes = (size_t)batch * num_kv_heads * (size_t)kv_len * head_dim * 2;
+  if (q_bytes && (!dout || !q || !o || !lse || !dq)) return GQA_ATTN_ERR_NULL_POINTER;
+  if (kv_bytes && (!k || !v || !dk || !dv)) return GQA_ATTN_ERR_NULL_POINTER;
+  if (((uintptr_t)dout | (uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)o |
+       (uintptr_t)lse | (uintptr_t)dlse | (uintptr_t)dq | (uintptr_t)dk | (uintptr_t)dv |
+       (uintptr_t)scratch) & 15u)
+    return GQA_ATTN_ERR_MISALIGNED;
+  const bool work = q_bytes && kv_bytes;
+  const size_t need = work ? bwd_scratch_bytes(s) : 0;
+  if (need && !scratch) return GQA_ATTN_ERR_NULL_POINTER;
+  if (scratch_bytes < need)
+    return detail(GQA_ATTN_ERR_ARG, "backward scratch of %zu bytes, needs %zu", scratch_bytes, need);
+  const void* outs[4] = {dq, dk, dv, scratch};
+  const size_t out_bytes[4] = {q_bytes, kv_bytes, kv_bytes, need};
+  const void* ins[7] = {dout, q, k, v, o, lse, dlse};
+  const size_t in_bytes[7] = {q_bytes, q_bytes, kv_bytes, kv_bytes, q_bytes, stat_bytes, stat_bytes};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 7; ++j)
+      if (overlaps(outs[i], out_bytes[i], ins[j], in_bytes[j])) return GQA_ATTN_ERR_ALIAS;
+    for (int j = 0; j < i; ++j)
+      if (overlaps(outs[i], out_bytes[i], outs[j], out_bytes[j])) return GQA_ATTN_ERR_ALIAS;
+  }
+  if (!q_bytes && !kv_bytes) return GQA_ATTN_OK;
+  int device = 0, sms = 0;
+  if ((rc = gqa_host::device(&device, &sms)) != GQA_ATTN_OK) return rc;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (!work) {  // no queries or no keys: every gradient that exists is zero
+    cudaError_t e = cudaSuccess;
+    if (q_bytes) e = cudaMemsetAsync(dq, 0, q_bytes, st);
+    if (kv_bytes) e = cudaMemsetAsync(dk, 0, kv_bytes, st);
+    if (kv_bytes && e == cudaSuccess) e = cudaMemsetAsync(dv, 0, kv_bytes, st);
+    return e == cudaSuccess ? GQA_ATTN_OK : cuda_fail("cudaMemsetAsync(gradient)", e, GQA_ATTN_ERR_LAUNCH);
+  }
+  p.q = (const __nv_bfloat16*)q;
+  p.k = (const __nv_bfloat16*)k;
+  p.v = (const __nv_bfloat16*)v;
+  p.dout = (const __nv_bfloat16*)dout;
+  p.dq = (__nv_bfloat16*)dq;
+  p.dk = (__nv_bfloat16*)dk;
+  p.dv = (__nv_bfloat16*)dv;
+  p.stats = (const float*)scratch;
+  p.softcap = softcap > 0.f;
+  p.scale = 1.0f / std::sqrt((float)head_dim);
+  p.logit_scale = kLog2e32 * p.scale;
+  p.cap_in = p.softcap ? p.scale / softcap : 0.f;
+  p.cap_out = p.softcap ? softcap * kLog2e32 : 0.f;
+  // Statistics: 16 rows a block, at most eight blocks (2048 threads) per SM.
+  const long long want = s.runs * s.tiles * 8;
+  const long long blocks = want < 8LL * sms ? want : 8LL * sms;
+  bwd_stats_kernel<<<(unsigned)blocks, 256, 0, st>>>(p.dout, (const __nv_bfloat16*)o, lse, dlse,
+                                                     (float*)scratch, s);
+  if ((rc = launched("launch(backward statistics)")) != GQA_ATTN_OK) return rc;
+  return head_dim <= 128 ? launch_bwd_mma<8>(p, device, st) : launch_bwd_mma<16>(p, device, st);
+}
+
+int gqa_attn_rotary(const void* q, const void* k, void* q_out, void* k_out, const void* positions,
+                    int batch, int length, int num_q_heads, int num_kv_heads, int head_dim,
+                    int num_axes, const int* sections, double theta, unsigned int flags,
+                    void* stream) {
+  if (flags & ~0xffu) return GQA_ATTN_ERR_ARG;
+  if (batch < 0 || length < 0 || num_q_heads < 0 || num_kv_heads < 0 ||
+      num_q_heads + (long long)num_kv_heads < 1)
+    return GQA_ATTN_ERR_BAD_SHAPE;
+  if (head_dim < 8 || head_dim > 256 || head_dim % 8 != 0) return GQA_ATTN_ERR_HEAD_DIM;
+  if (num_axes < 1 || num_axes > kRotMaxAxes || !sections)
+    return detail(GQA_ATTN_ERR_ARG, "rotary: %d axes, takes 1 to %d", num_axes, kRotMaxAxes);
+  if (!(theta > 0.0) || std::isinf(theta)) return detail(GQA_ATTN_ERR_ARG, "rotary: theta %g", theta);
+  long long pairs = 0;
+  for (int a = 0; a < num_axes; ++a) {
+    if (sections[a] < 1) return detail(GQA_ATTN_ERR_ARG, "rotary: section of %d pairs", sections[a]);
+    pairs += sections[a];
+  }
+  if (2 * pairs > head_dim)
+    return detail(GQA_ATTN_ERR_ARG, "rotary: %lld pairs in a head of %d", pairs, head_dim);
+  const bool in32 = flags & GQA_ROTARY_IN_F32, out32 = flags & GQA_ROTARY_OUT_F32;
+  const bool in_seq = flags & GQA_ROTARY_IN_SEQ_MAJOR, out_seq = flags & GQA_ROTARY_OUT_SEQ_MAJOR;
+  const bool interleaved = flags & GQA_ROTARY_INTERLEAVED;
+  const long long tokens = (long long)batch * length;
+  const long long heads = (long long)num_q_heads + num_kv_heads;
+  if (heads > 65535 || tokens > (1LL << 38)) return GQA_ATTN_ERR_TOO_LARGE;
+  const size_t n[2] = {(size_t)tokens * num_q_heads * head_dim, (size_t)tokens * num_kv_heads * head_dim};
+  const void* in[2] = {q, k};
+  void* out[2] = {q_out, k_out};
+  if (tokens && !positions) return GQA_ATTN_ERR_NULL_POINTER;
+  if (((uintptr_t)positions | (uintptr_t)q | (uintptr_t)k | (uintptr_t)q_out | (uintptr_t)k_out) & 15u)
+    return GQA_ATTN_ERR_MISALIGNED;
+  const size_t ie = in32 ? 4 : 2, oe = out32 ? 4 : 2;
+  const size_t pos_bytes = (size_t)num_axes * (size_t)tokens * ((flags & GQA_ROTARY_POS_I64) ? 8 : 4);
+  for (int w = 0; w < 2; ++w) {
+    if (n[w] && (!in[w] || !out[w])) return GQA_ATTN_ERR_NULL_POINTER;
+    if (overlaps(out[w], n[w] * oe, positions, pos_bytes)) return GQA_ATTN_ERR_ALIAS;
+    // In place is fine where every element stays where it is.
+    if (!(out[w] == in[w] && in32 == out32 && in_seq == out_seq) &&
+        overlaps(out[w], n[w] * oe, in[w], n[w] * ie))
+      return GQA_ATTN_ERR_ALIAS;
+    if (overlaps(out[w], n[w] * oe, in[1 - w], n[1 - w] * ie)) return GQA_ATTN_ERR_ALIAS;
+  }
+  if (overlaps(q_out, n[0] * oe, k_out, n[1] * oe)) return GQA_ATTN_ERR_ALIAS;
+  if (tokens == 0) return GQA_ATTN_OK;
+  int device = 0, sms = 0;
+  const int rc = gqa_host::device(&device, &sms);
+  if (rc != GQA_ATTN_OK) return rc;
+  RotaryParams p;
+  p.q = q;
+  p.k = k;
+  p.q_out = q_out;
+  p.k_out = k_out;
+  p.positions = positions;
+  p.pos64 = (flags & GQA_ROTARY_POS_I64) ? 1 : 0;
+  p.inverse = (flags & GQA_ROTARY_INVERSE) ? 1 : 0;
+  p.batch = batch;
+  p.length = length;
+  p.head_dim = head_dim;
+  p.q_heads = num_q_heads;
+  p.kv_heads = num_kv_heads;
+  p.pairs = (int)pairs;
+  // Strides of the dense [batch][length][heads][d] and [batch][heads][length][d].
+  for (int w = 0; w < 2; ++w) {
+    const long long h = w ? num_kv_heads : num_q_heads, d = head_dim;
+    p.in_b[w] = p.out_b[w] = h * length * d;
+    p.in_h[w] = in_seq ? d : (long long)length * d;
+    p.in_l[w] = in_seq ? h * d : d;
+    p.out_h[w] = out_seq ? d : (long long)length * d;
+    p.out_l[w] = out_seq ? h * d : d;
+  }
+  // Frequency of pair i: theta^(-i / pairs), or theta^(-j / section) for the
+  // j-th pair of its axis, as turns per position.
+  const double pi2 = 6.283185307179586476925286766559;
+  int at = 0;
+  for (int a = 0; a < num_axes; ++a)
+    for (int j = 0; j < sections[a]; ++j, ++at) {
+      const double e = (flags & GQA_ROTARY_PER_AXIS) ? (double)j / sections[a] : (double)at / (double)pairs;
+      p.turn[at] = std::pow(theta, -e) / pi2;
+      p.axis[at] = (unsigned char)a;
+    }
+  // The widest vector that keeps every access aligned: 8 bf16 (16 bytes) or
+  // 4 elements when the pairs divide by it, else single elements.
+  const int v = pairs % 8 == 0 && !in32 && !out32 && !interleaved ? 8 : pairs % 4 == 0 ? 4 : 1;
+  p.vecs = ((int)pairs + (head_dim - 2 * (int)pairs)) / v;
+  // All heads of a token in one thread, unless that leaves the SMs short of
+  // threads: then runs of heads, down to a single one.
+  const long long threads = tokens * p.vecs;
+  const long long runs = ceil_div((long long)sms * 1024, threads);
+  p.heads_per_thread = (int)(runs >= heads ? 1 : ceil_div(heads, runs));
+  const long long gx = ceil_div(threads, kRotThreads);
+  if (gx > 0x7fffffffLL) return GQA_ATTN_ERR_TOO_LARGE;
+  const dim3 grid((unsigned)gx, (unsigned)ceil_div(heads, p.heads_per_thread));
+  cudaStream_t st = (cudaStream_t)stream;
+  if (v == 8) {
+    rotary_kernel<8, __nv_bfloat16, __nv_bfloat16, false><<<grid, kRotThreads, 0, st>>>(p);
+    return launched("launch(rotary)");
+  }
+  if (v == 4) return launch_rotary_types<4>(p, in32, out32, interleaved, grid, st);
+  return launch_rotary_types<1>(p, in32, out32, interleaved, grid, st);
+}
+
+}  // extern "C"

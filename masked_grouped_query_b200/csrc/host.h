@@ -1,0 +1,35 @@
+// host.h -- host-side pieces that gqa_attn.cu offers to the library's other
+// translation unit.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace gqa_host {
+
+// The current device: checked for compute capability 10.x (GQA_ATTN_ERR_DEVICE
+// otherwise); *index gets its number, *sms its SM count.
+int device(int* index, int* sms);
+
+// 3-D bf16 tensor map over [outer][rows][cols] with a (64 cols x box_rows x 1)
+// box and 128-byte swizzle; out-of-range elements read as zero.
+int tensor_map(CUtensorMap* map, const void* base, int cols, long long rows, long long outer,
+               int box_rows);
+
+// Value of the force_path override (0 automatic, 1 mma.sync, 2 tcgen05).
+int forced_path();
+
+// Remember a failed CUDA call for gqa_attn_last_error_detail; returns `code`.
+int cuda_fail(const char* where, cudaError_t e, int code);
+// The same for a message of this library.
+int detail(int code, const char* fmt, ...);
+
+bool overlaps(const void* a, size_t na, const void* b, size_t nb);
+
+// Defined in gqa_train.cu: its status word (returns a CUDA error).
+cudaError_t train_status(uint32_t* word);
+cudaError_t train_clear_status();
+
+}  // namespace gqa_host

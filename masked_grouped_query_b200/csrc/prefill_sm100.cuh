@@ -113,7 +113,14 @@ struct PrefillParams {
   float* ws_o;
   float* ws_ml;
   unsigned int* tickets;
+  float* lse;  // kLse kernels: log-sum-exp per row, natural logarithm ([unit][row])
 };
+
+// Natural-log log-sum-exp of a row from its base and sum in log2 units
+// (-inf for a row without a visible key).
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
 
 template <int DCH>
 struct PrefillCfg {
@@ -298,8 +305,13 @@ __device__ __forceinline__ int key_tile(const PfItem& it, int t, int j) {
 // partials the last CTA of a unit merges (tickets); 2 = paired splits, one
 // item per CTA, merged by the unit's thread-block cluster.  Both keep their
 // partials in the workspace.  Each kernel holds only its own merge code:
-// the ticket merge alone made the clustered kernel slower.
-template <int DCH, int kCapDeg, int kSplit>
+// the ticket merge alone made the clustered kernel slower.  kLse: also
+// returns every row's log-sum-exp in fp32.  Those kernels spend what the
+// others save at an error below the bf16 output's rounding: every 2^x on
+// MUFU (2^-22 relative; the FMA-pipe cubic has 7.5e-5) and an accurate tanh
+// (degree 9, or 1 - 2 / (1 + e^2y)).  They exist with kCapDeg 0 and 7 only,
+// and merge splits by ticket.
+template <int DCH, int kCapDeg, int kSplit, bool kLse = false>
 __global__ void __launch_bounds__(kPfThreads, 1)
     prefill_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
                          const __grid_constant__ CUtensorMap tm_k,
@@ -842,7 +854,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
               const f2 y = logit2(f2_pack(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1])));
-              f2 pv = (!kCap && c >= kEmuFrom) ? exp2_poly_x2(y) : exp2_mufu_x2(y);
+              f2 pv = (!kCap && !kLse && c >= kEmuFrom) ? exp2_poly_x2(y) : exp2_mufu_x2(y);
               if constexpr (kHid) {
                 float a, b;
                 f2_unpack(pv, a, b);
@@ -893,6 +905,18 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               const f2 v2 = f2_mul(v, v);
               return f2_fma(v, f2_fma(f2_fma(q2, v2, q1), v2, q0), nb);
             }, No());
+          } else if constexpr (kLse) {
+            const f2 q0 = f2_pack(cc * kTanh9C1, cc * kTanh9C1);
+            const f2 q1 = f2_pack(cc * ci2 * kTanh9C3, cc * ci2 * kTanh9C3);
+            const f2 q2 = f2_pack(cc * ci2 * ci2 * kTanh9C5, cc * ci2 * ci2 * kTanh9C5);
+            const float ci6 = ci2 * ci2 * ci2;
+            const f2 q3 = f2_pack(cc * ci6 * kTanh9C7, cc * ci6 * kTanh9C7);
+            const f2 q4 = f2_pack(cc * ci6 * ci2 * kTanh9C9, cc * ci6 * ci2 * kTanh9C9);
+            emit([&](f2 v) {
+              const f2 v2 = f2_mul(v, v);
+              return f2_fma(
+                  v, f2_fma(f2_fma(f2_fma(f2_fma(q4, v2, q3), v2, q2), v2, q1), v2, q0), nb);
+            }, Yes());
           } else {
             const f2 q0 = f2_pack(cc * kTanhC1, cc * kTanhC1);
             const f2 q1 = f2_pack(cc * ci2 * kTanhC3, cc * ci2 * kTanhC3);
@@ -909,6 +933,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           emit([&](f2 v) {
             float a, b;
             f2_unpack(v, a, b);
+            if constexpr (kLse)
+              return f2_pack(fmaf(co, tanh_accurate(a * ci), -base),
+                             fmaf(co, tanh_accurate(b * ci), -base));
             return f2_pack(fmaf(co, tanh_fast(a * ci), -base), fmaf(co, tanh_fast(b * ci), -base));
           }, Yes());
         }
@@ -979,6 +1006,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           const bool have = act > 0;  // warp-uniform
           const bool live = have && m != -INFINITY && l > 0.f;
           const float inv = live ? 1.0f / l : 0.f;
+          if constexpr (kLse)
+            if (r < ti.nrows)
+              p.lse[(long long)it.unit * p.rows + ti.row0 + r] = row_lse(m, live ? l : 0.f);
           for (int c0 = 0; c0 < p.d_pad; c0 += 64)
             store_box(ti, c0, [&](int col, float (&v)[16]) {
               if (have) {
@@ -1108,6 +1138,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               const int nch = (cw1 - cw0) / 16;
               const int cb = cw0 + 16 * (nch * part / parts);
               const int ce = cw0 + 16 * (nch * (part + 1) / parts);
+              // The last part has columns whenever the warpgroup has.
+              const bool write_lse = kLse && part == parts - 1 && cw0 == 0;
               if (rg < nq && cb < ce) {
                 const int row = rg * 32 + lane;  // < 128: partial rows past nrows exist
                 // Row max and row sum over the partials in one pass, eight
@@ -1134,6 +1166,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                   }
                 }
                 const float inv = Ls > 0.f ? 1.0f / Ls : 0.f;
+                if (write_lse && row < wt.nrows)
+                  p.lse[(long long)it.unit * p.rows + wt.row0 + row] = row_lse(M, Ls);
                 __nv_bfloat16* orow =
                     p.o + ((long long)it.unit * p.rows + wt.row0 + row) * p.head_dim;
                 for (int col = cb; col < ce; col += 16) {

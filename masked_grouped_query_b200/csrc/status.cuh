@@ -23,8 +23,9 @@ enum : uint32_t {
 // Two seconds: far above any legitimate wait in these kernels.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
-// Defined here: the library is compiled as a single translation unit.
-__device__ uint32_t g_gqa_status = 0;
+// One word per translation unit (gqa_attn.cu, gqa_train.cu); gqa_attn_status
+// reads both.
+static __device__ uint32_t g_gqa_status = 0;
 
 __device__ __forceinline__ void report_status(uint32_t code) { atomicOr(&g_gqa_status, code); }
 
