@@ -15,6 +15,7 @@
 #include "ptx.cuh"
 #include "mask.cuh"
 #include "backward.cuh"
+#include "backward_sm100.cuh"
 #include "rotary.cuh"
 
 namespace {
@@ -92,6 +93,54 @@ int launch_bwd_mma(const BwdParams& p, int device, cudaStream_t st) {
   if ((rc = launched("launch(backward dK dV)")) != GQA_ATTN_OK) return rc;
   const long long row_tiles = p.sh.runs * ceil_div(p.sh.run, kBmTile);
   bwd_mma_kernel<KS, true><<<(unsigned)row_tiles, kBmThreads, C::kSmemBytes, st>>>(p);
+  return launched("launch(backward dQ)");
+}
+
+// Shared memory limit of a tcgen05 backward kernel, and the check that its
+// register split fits what the block is launched with (setmaxnreg.inc could
+// never be granted otherwise).
+template <typename K>
+int bwd_sm100_setup(K kernel, int bytes, int device, bool* done) {
+  {
+    std::lock_guard<std::mutex> lk(g_attr_mu);
+    if (done[device]) return GQA_ATTN_OK;
+  }
+  cudaFuncAttributes fa;
+  const cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
+  if (e != cudaSuccess) return cuda_fail("cudaFuncGetAttributes(backward)", e, GQA_ATTN_ERR_LAUNCH);
+  if (fa.numRegs * kBwThreads < kBwRegTotal)
+    return detail(GQA_ATTN_ERR_LAUNCH, "backward kernel built with %d registers/thread: register "
+                  "split needs %d", fa.numRegs, kBwRegTotal);
+  return allow_smem(kernel, bytes, device, done);
+}
+
+template <int DCH, bool kCap>
+int launch_bwd_sm100(const BwdParams& p, int device, cudaStream_t st) {
+  using C = BwdCfg<DCH>;
+  static bool done_kv[kMaxDevices], done_q[kMaxDevices];
+  int rc = bwd_sm100_setup(bwd_dkdv_kernel<DCH, kCap>, C::kSmemBytes, device, done_kv);
+  if (rc == GQA_ATTN_OK) rc = bwd_sm100_setup(bwd_dq_kernel<DCH, kCap>, C::kSmemBytes, device, done_q);
+  if (rc != GQA_ATTN_OK) return rc;
+  const BwdShape& s = p.sh;
+  CUtensorMap q, dout, k, v, dq, dk, dv;
+  const struct {
+    CUtensorMap* map;
+    const void* base;
+    bool rows;
+    int box;
+  } maps[7] = {{&q, p.q, true, 128},     {&dout, p.dout, true, 128}, {&k, p.k, false, 128},
+               {&v, p.v, false, 128},    {&dq, p.dq, true, 32},      {&dk, p.dk, false, 32},
+               {&dv, p.dv, false, 32}};
+  for (const auto& m : maps)
+    if ((rc = gqa_host::tensor_map(m.map, m.base, s.head_dim, m.rows ? s.run : s.kv_len,
+                                   m.rows ? s.runs : s.units, m.box)) != GQA_ATTN_OK)
+      return rc;
+  const long long key_tiles = s.units * ceil_div(s.kv_len, 128);
+  bwd_dkdv_kernel<DCH, kCap><<<(unsigned)key_tiles, kBwThreads, C::kSmemBytes, st>>>(q, dout, k, v, dk,
+                                                                                  dv, p);
+  if ((rc = launched("launch(backward dK dV)")) != GQA_ATTN_OK) return rc;
+  bwd_dq_kernel<DCH, kCap><<<(unsigned)(s.runs * s.tiles), kBwThreads, C::kSmemBytes, st>>>(q, dout, k,
+                                                                                         v, dq, p);
   return launched("launch(backward dQ)");
 }
 
@@ -206,7 +255,15 @@ int gqa_attn_bwd(const void* dout, const void* q, const void* k, const void* v, 
   bwd_stats_kernel<<<(unsigned)blocks, 256, 0, st>>>(p.dout, (const __nv_bfloat16*)o, lse, dlse,
                                                      (float*)scratch, s);
   if ((rc = launched("launch(backward statistics)")) != GQA_ATTN_OK) return rc;
-  return head_dim <= 128 ? launch_bwd_mma<8>(p, device, st) : launch_bwd_mma<16>(p, device, st);
+  // The tcgen05 kernels hold dK and dV of 128 columns each in TMEM next to the
+  // scores: wider heads stay on mma.sync (force_path 1 does for every width).
+  if (head_dim > 128) return launch_bwd_mma<16>(p, device, st);
+  if (gqa_host::forced_path() == 1) return launch_bwd_mma<8>(p, device, st);
+  if (head_dim <= 64)
+    return p.softcap ? launch_bwd_sm100<1, true>(p, device, st)
+                     : launch_bwd_sm100<1, false>(p, device, st);
+  return p.softcap ? launch_bwd_sm100<2, true>(p, device, st)
+                   : launch_bwd_sm100<2, false>(p, device, st);
 }
 
 int gqa_attn_rotary(const void* q, const void* k, void* q_out, void* k_out, const void* positions,
