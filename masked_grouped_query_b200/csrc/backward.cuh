@@ -43,7 +43,7 @@ struct BwdParams {
   BwdShape sh;
   const __nv_bfloat16 *q, *k, *v, *dout;
   __nv_bfloat16 *dq, *dk, *dv;
-  const float* stats;  // [run][tile]: 128 lse (log2 units, +inf: no key), then 128 delta
+  const float* stats;  // [run][tile]: 128 times -lse (log2 units, -inf: no key), then 128 delta
   int softcap;
   float scale;         // 1 / sqrt(D)
   float logit_scale;   // log2(e) / sqrt(D)
@@ -90,7 +90,7 @@ __host__ __device__ __forceinline__ void bwd_row_tiles(const BwdShape& s, int k0
 
 // delta and lse of every row into the tiled statistics: a group of 16
 // threads per row, 16-byte loads.  Rows that pad a run's last tile get
-// lse = +inf and delta = 0, so that their P and dS are zero.  Bound by the
+// -lse = -inf and delta = 0, so that their P and dS are zero.  Bound by the
 // reads of dO and O.
 __global__ void __launch_bounds__(256)
     bwd_stats_kernel(const __nv_bfloat16* __restrict__ dout, const __nv_bfloat16* __restrict__ o,
@@ -125,10 +125,10 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int i = 8; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i, 16);
     if (part == 0) {
-      float l2 = INFINITY;
+      float l2 = -INFINITY;
       if (live) {
         const float l = lse[row];
-        l2 = l == -INFINITY ? INFINITY : l * kLog2e32;
+        l2 = l == -INFINITY ? -INFINITY : -l * kLog2e32;
         if (dlse) sum -= dlse[row];
       }
       stats[tile * 256 + r] = l2;
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kBmThreads, 1) bwd_mma_kernel(const BwdParams 
   __nv_bfloat16* str2 = str1 + C::kTileElems;      // dO or V
   __nv_bfloat16* pm = str2 + C::kTileElems;        // P  [own row][streamed row]
   __nv_bfloat16* dm = pm + kBmTile * C::kPPitch;   // dS
-  float* st = (float*)(dm + kBmTile * C::kPPitch); // 64 lse, 64 delta of the query rows
+  float* st = (float*)(dm + kBmTile * C::kPPitch); // 64 times -lse, 64 delta of the query rows
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t4 = lane & 3, mi = lane >> 3, rr = lane & 7;
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kBmThreads, 1) bwd_mma_kernel(const BwdParams 
           } else {
             y = x * p.logit_scale;
           }
-          const float pr = see ? ex2(y - st[qr]) : 0.f;
+          const float pr = see ? ex2(y + st[qr]) : 0.f;
           const float d = pr * (dp[n][2 * h + e] - st[64 + qr]) * (1.f - t * t);
           pv[e] = pr;
           dv[e] = see ? d : 0.f;

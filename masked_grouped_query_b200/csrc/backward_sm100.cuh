@@ -4,7 +4,7 @@
 // Two kernels with the same frame, one CTA of 12 warps per tile of 128 and
 // per SM:
 //   warp 0      TMA loader (and the statistics' bulk copies);
-//   warp 1      TMEM allocator, and the thread that issues every tcgen05.mma;
+//   warp 1      TMEM allocator; its lane 0 issues every tcgen05.mma;
 //   warps 2-3   idle (they complete warpgroup 0 for the register split);
 //   warps 4-11  elementwise work: warpgroup h takes columns [64 h, 64 h + 64)
 //               of the 128 x 128 tiles, a thread one lane (row) of them.
@@ -81,20 +81,20 @@ __device__ __forceinline__ bool bwd_need_mask(const BwdShape& s, const MaskSpec&
   return !(k0 >= first_key(ms, base + i1) && k0 + 127 <= last_key(ms, base + i0));
 }
 
-// P of 32 columns from 32 raw scores: 2^(x - lse), and with a softcap the
-// factor (1 - tanh^2) for dS folded into `keep` (else keep = p).
+// P of 32 columns from 32 raw scores (nl: -lse of their rows, in pairs), and
+// with a softcap the factors 1 - tanh^2 that dS takes.  The last pairs of
+// every 16 take 2^x from the FMA pipe: MUFU alone would need 1024 cycles for
+// a 128 x 128 tile, half of the tensor core's time for the tile's products.
+constexpr int kBwEmuFrom = 13;
 template <bool kCap>
 __device__ __forceinline__ void bwd_probs(const BwdParams& p, const uint32_t (&s)[32],
-                                          const float (&lse)[32], float (&pr)[32], float* keep) {
+                                          const f2 (&nl)[16], f2 (&pr)[16], f2 (&fac)[16]) {
   if constexpr (!kCap) {
     const f2 sc = f2_pack(p.logit_scale, p.logit_scale);
 #pragma unroll
-    for (int c = 0; c < 32; c += 2) {
-      const f2 y = f2_fma(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc,
-                          f2_pack(-lse[c], -lse[c + 1]));
-      f2_unpack(exp2_mufu_x2(y), pr[c], pr[c + 1]);
-      keep[c] = pr[c];
-      keep[c + 1] = pr[c + 1];
+    for (int c = 0; c < 16; ++c) {
+      const f2 y = f2_fma(f2_pack(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), sc, nl[c]);
+      pr[c] = c >= kBwEmuFrom ? exp2_poly_x2(y) : exp2_mufu_x2(y);
     }
   } else {
     float am = 0.f;
@@ -102,21 +102,61 @@ __device__ __forceinline__ void bwd_probs(const BwdParams& p, const uint32_t (&s
     for (int c = 0; c < 32; c += 2)
       am = fmax3(am, fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
     const bool small = __all_sync(0xffffffffu, am * p.cap_in <= 0.5f);
+    const f2 co = f2_pack(p.cap_out, p.cap_out), one = f2_pack(1.f, 1.f);
     if (small) {
+      const f2 ci = f2_pack(p.cap_in, p.cap_in), nci = f2_pack(-p.cap_in, -p.cap_in);
+      const f2 c3 = f2_pack(kTanh9C3, kTanh9C3), c5 = f2_pack(kTanh9C5, kTanh9C5);
+      const f2 c7 = f2_pack(kTanh9C7, kTanh9C7), c9 = f2_pack(kTanh9C9, kTanh9C9);
 #pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        const float t = tanh_poly9_small(__uint_as_float(s[c]) * p.cap_in);
-        pr[c] = ex2(fmaf(p.cap_out, t, -lse[c]));
-        keep[c] = pr[c] * fmaf(-t, t, 1.f);
+      for (int c = 0; c < 16; ++c) {
+        const f2 x = f2_pack(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
+        const f2 y = f2_mul(x, ci), y2 = f2_mul(y, y);
+        const f2 q = f2_fma(f2_fma(f2_fma(f2_fma(c9, y2, c7), y2, c5), y2, c3), y2, one);
+        const f2 t = f2_mul(y, q);
+        pr[c] = exp2_mufu_x2(f2_fma(co, t, nl[c]));
+        fac[c] = f2_fma(t, f2_mul(f2_mul(x, nci), q), one);
       }
     } else {
 #pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        const float t = tanh_accurate(__uint_as_float(s[c]) * p.cap_in);
-        pr[c] = ex2(fmaf(p.cap_out, t, -lse[c]));
-        keep[c] = pr[c] * fmaf(-t, t, 1.f);
+      for (int c = 0; c < 16; ++c) {
+        const float a = tanh_accurate(__uint_as_float(s[2 * c]) * p.cap_in);
+        const float b = tanh_accurate(__uint_as_float(s[2 * c + 1]) * p.cap_in);
+        pr[c] = exp2_mufu_x2(f2_fma(co, f2_pack(a, b), nl[c]));
+        fac[c] = f2_pack(fmaf(-a, a, 1.f), fmaf(-b, b, 1.f));
       }
     }
+  }
+}
+
+// dS of 32 columns as bf16 from what bwd_probs left (p times the factor), dP
+// and the rows' delta.  A hidden score is an exact zero whatever dP is.
+__device__ __forceinline__ void bwd_ds(const f2* keep, const uint32_t (&dp)[32], const f2 (&dl)[16],
+                                       bool masked, uint32_t (&pk)[16]) {
+  f2 d[16];
+#pragma unroll
+  for (int c = 0; c < 16; ++c)
+    d[c] = f2_mul(keep[c], f2_sub(f2_pack(__uint_as_float(dp[2 * c]), __uint_as_float(dp[2 * c + 1])),
+                                  dl[c]));
+  if (masked) {
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      float k0, k1, a, b;
+      f2_unpack(keep[c], k0, k1);
+      f2_unpack(d[c], a, b);
+      d[c] = f2_pack(k0 == 0.f ? 0.f : a, k1 == 0.f ? 0.f : b);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < 16; ++c) pk[c] = pack_bf16_f2(d[c]);
+}
+
+// 32 floats of shared memory, the same for every lane, as pairs.
+__device__ __forceinline__ void bwd_load32(const float* src, f2 (&v)[16]) {
+#pragma unroll
+  for (int c = 0; c < 16; c += 2) {
+    const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(src + 2 * c);
+    v[c] = w.x;
+    v[c + 1] = w.y;
   }
 }
 
@@ -156,31 +196,39 @@ __device__ __forceinline__ void bwd_store_box(const CUtensorMap* map, uint8_t* s
   }
 }
 
-// The products' issue loops.  A and B K-major from shared memory (128 x 128,
-// K = head_dim):
+// The products, 8 K-steps of 16 unless K is head_dim.  Shared memory lies
+// below 256 KB, so a descriptor's 14-bit address field never carries out and
+// a K-step is one addition to its low word.
+// A and B K-major from shared memory (128 x 128, K = head_dim):
 template <int DCH>
-__device__ __forceinline__ void bwd_issue_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
-                                             int ksteps) {
+__device__ __forceinline__ void bwd_issue_ss(uint32_t leader, uint32_t d, uint64_t ad, uint64_t bd,
+                                             uint32_t idesc, int ksteps) {
   using C = BwdCfg<DCH>;
-  const uint64_t ad = sdesc_sw128(a, 16, 1024), bd = sdesc_sw128(b, 16, 1024);
 #pragma unroll
   for (int ks = 0; ks < 4 * DCH; ++ks) {
     if (ks >= ksteps) break;
-    const uint32_t off = (ks >> 2) * C::kBoxBytes + (ks & 3) * 32;
-    mma_bf16_ss(d, sdesc_advance(ad, off), sdesc_advance(bd, off), idesc, ks > 0);
+    const uint32_t off = ((ks >> 2) * C::kBoxBytes + (ks & 3) * 32) >> 4;
+    mma_bf16_ss_warp(leader, d, ad + off, bd + off, idesc, ks > 0);
   }
 }
 // A (128 x 128 bf16) from TMEM: columns 0..63 of the tile at a, 64..127 at
-// a + 64; B (128 x N) from shared memory, N contiguous.
-template <int DCH>
-__device__ __forceinline__ void bwd_issue_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
-                                             bool first) {
-  using C = BwdCfg<DCH>;
-  const uint64_t bd = sdesc_sw128(b, C::kBoxBytes, 1024);
+// a + 64; B (128 x N) from shared memory, N contiguous.  K-steps [k0, k1) of
+// both halves.
+__device__ __forceinline__ void bwd_issue_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t bd,
+                                             uint32_t idesc, bool first, int k0, int k1) {
 #pragma unroll
-  for (int ks = 0; ks < 8; ++ks)
-    mma_bf16_ts(d, a + (ks >> 2) * 64 + (ks & 3) * 8, sdesc_advance(bd, ks * 2048), idesc,
-                !(first && ks == 0));
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int ks = k0; ks < k1; ++ks)
+      mma_bf16_ts_warp(leader, d, a + h * 64 + ks * 8, bd + (4 * h + ks) * (2048 >> 4), idesc,
+                       !(first && h == 0 && ks == 0));
+}
+// Descriptors of a tile as either operand of bwd_issue_ss, and as the B of
+// bwd_issue_ts.
+__device__ __forceinline__ uint64_t bwd_desc_k(uint32_t tile) { return sdesc_sw128(tile, 16, 1024); }
+template <int DCH>
+__device__ __forceinline__ uint64_t bwd_desc_n(uint32_t tile) {
+  return sdesc_sw128(tile, BwdCfg<DCH>::kBoxBytes, 1024);
 }
 
 // ------------------------------------------------------------------ dK, dV
@@ -211,9 +259,10 @@ __global__ void __launch_bounds__(kBwThreads, 1)
   uint64_t* p_full = bars + 17;
   uint64_t* ds_full = bars + 18;
   uint64_t* o_done = bars + 19;
+  uint64_t* p_half = bars + 20;
   uint32_t* tmem_slot = (uint32_t*)(bars + C::kNumBars);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
     for (int i = 0; i < 3; ++i) {
@@ -228,6 +277,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
     }
     mbar_init(s_full, 1);
     mbar_init(dp_full, 1);
+    mbar_init(p_half, 8);
     mbar_init(p_full, 8);
     mbar_init(ds_full, 8);
     mbar_init(o_done, 1);
@@ -296,42 +346,59 @@ __global__ void __launch_bounds__(kBwThreads, 1)
         mbar_wait(&st_full[j & 1], (j / 2) & 1, kStatusTimeoutProducer);
     }
   } else if (warp == 1) {
-    if (lane == 0 && n > 0) {
+    // The whole warp walks the loop, lane 0 issues (see mma_bf16_ss_warp).
+    if (n > 0) {
+      const uint32_t leader = lane == 0;
       const int d_pad = (s.head_dim + 15) / 16 * 16, ksteps = d_pad / 16;
       const uint32_t idesc_s = idesc_bf16_f32(128, 128, 0);
       const uint32_t idesc_o = idesc_bf16_f32(128, d_pad, 1);
-      const uint32_t ka = smem_u32(sk), va = smem_u32(sv), qa = smem_u32(sq), da = smem_u32(sdo);
-      constexpr uint32_t code = kStatusTimeoutMma;
-      bool ok = mbar_wait(kv_full, 0, code) && mbar_wait(&q_full[0], 0, code);
+      const uint64_t kd = bwd_desc_k(smem_u32(sk)), vd = bwd_desc_k(smem_u32(sv));
+      const uint64_t qk = bwd_desc_k(smem_u32(sq)), qn = bwd_desc_n<DCH>(smem_u32(sq));
+      const uint64_t dk = bwd_desc_k(smem_u32(sdo)), dn = bwd_desc_n<DCH>(smem_u32(sdo));
+      constexpr uint32_t kTile = C::kTileBytes >> 4;  // a slot, in descriptor units
+      // Uniform over the warp, so that it stays converged.
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, kStatusTimeoutMma)) != 0;
+      };
+      bool ok = wait(kv_full, 0) && wait(&q_full[0], 0);
       if (ok) {
         tc_fence_after();
-        bwd_issue_ss<DCH>(tmem, ka, qa, idesc_s, ksteps);
-        mma_commit(s_full);
+        bwd_issue_ss<DCH>(leader, tmem, kd, qk, idesc_s, ksteps);
+        mma_commit_warp(leader, s_full);
       }
+      int sq_j = 0, sq_n = 1;  // Q slots of tiles j and j + 1
+      ok = ok && wait(&do_full[0], 0);
       for (int j = 0; j < n && ok; ++j) {
-        const uint32_t doj = da + (j & 1) * C::kTileBytes;
-        if (!(ok = mbar_wait(&do_full[j & 1], (j / 2) & 1, code))) break;
+        const uint32_t doj = (j & 1) * kTile;
+        const bool more = j + 1 < n;
         tc_fence_after();
-        bwd_issue_ss<DCH>(tmem + 128, va, doj, idesc_s, ksteps);
-        mma_commit(dp_full);
-        if (!(ok = mbar_wait(p_full, j & 1, code))) break;
+        bwd_issue_ss<DCH>(leader, tmem + 128, vd, dk + doj, idesc_s, ksteps);
+        mma_commit_warp(leader, dp_full);
+        // dV in two parts: rows 0..31 and 64..95 of the tile first.
+        if (!(ok = wait(p_half, j & 1))) break;
         tc_fence_after();
-        bwd_issue_ts<DCH>(tmem + 256, tmem, doj, idesc_o, j == 0);
-        mma_commit(&do_empty[j & 1]);
-        if (j + 1 < n) {
-          if (!(ok = mbar_wait(&q_full[(j + 1) % 3], ((j + 1) / 3) & 1, code))) break;
-          tc_fence_after();
-          bwd_issue_ss<DCH>(tmem, ka, qa + (j + 1) % 3 * C::kTileBytes, idesc_s, ksteps);
-          mma_commit(s_full);
+        bwd_issue_ts(leader, tmem + 256, tmem, dn + doj, idesc_o, j == 0, 0, 2);
+        // The next tile's operands are waited for ahead of their turn.
+        if (more && !(ok = wait(&q_full[sq_n], ((j + 1) / 3) & 1))) break;
+        if (!(ok = wait(p_full, j & 1))) break;
+        tc_fence_after();
+        bwd_issue_ts(leader, tmem + 256, tmem, dn + doj, idesc_o, false, 2, 4);
+        mma_commit_warp(leader, &do_empty[j & 1]);
+        if (more) {
+          bwd_issue_ss<DCH>(leader, tmem, kd, qk + sq_n * kTile, idesc_s, ksteps);
+          mma_commit_warp(leader, s_full);
+          if (!(ok = wait(&do_full[(j + 1) & 1], ((j + 1) / 2) & 1))) break;
         }
-        if (!(ok = mbar_wait(ds_full, j & 1, code))) break;
+        if (!(ok = wait(ds_full, j & 1))) break;
         tc_fence_after();
-        bwd_issue_ts<DCH>(tmem + 384, tmem + 128, qa + j % 3 * C::kTileBytes, idesc_o, j == 0);
-        mma_commit(&q_empty[j % 3]);
+        bwd_issue_ts(leader, tmem + 384, tmem + 128, qn + sq_j * kTile, idesc_o, j == 0, 0, 4);
+        mma_commit_warp(leader, &q_empty[sq_j]);
+        sq_j = sq_n;
+        if (++sq_n == 3) sq_n = 0;
       }
       // Every product finished before the epilogue, and before TMEM is freed.
-      mma_commit(o_done);
-      mbar_wait(o_done, 0, code);
+      mma_commit_warp(leader, o_done);
+      wait(o_done, 0);
     }
   } else if (warp >= 4) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kBwRegsHigh));
@@ -353,82 +420,70 @@ __global__ void __launch_bounds__(kBwThreads, 1)
     for (int j = 0; j < n; ++j) {
       const int r0 = t * 128, nr = min(128, s.run - r0);
       const bool need_mask = bwd_need_mask(s, ms, r0, nr, k0);
-      float pr[64];
+      f2 keep[32];
       const float* st = stats + (j & 1) * 256 + 64 * h;
       ok = mbar_wait(&st_full[j & 1], (j / 2) & 1, kStatusTimeoutSoftmax) &&
            mbar_wait(s_full, j & 1, kStatusTimeoutSoftmax);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
+      uint32_t b0[32], b1[32];
+      tmem_ld32(s_tm, b0);
       int qi = need_mask ? (r0 + 64 * h) % s.q_len : 0;  // query of the next column
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        uint32_t sv32[32];
-        float lse[32], pc[32];
-        tmem_ld32(s_tm + 32 * g, sv32);
-#pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(st + 32 * g + c);
-          lse[c] = f.x;
-          lse[c + 1] = f.y;
-          lse[c + 2] = f.z;
-          lse[c + 3] = f.w;
-        }
-        tmem_ld_wait();
-        bwd_probs<kCap>(p, sv32, lse, pc, &pr[32 * g]);
+      // P of columns 32 g .. 32 g + 31 of this half, into TMEM columns
+      // [16 g, 16 g + 16) of it, whose scores have been read.
+      auto probs = [&](const uint32_t(&sv32)[32], int g) {
+        f2 nl[16], pr[16], fac[16];
+        bwd_load32(st + 32 * g, nl);
+        bwd_probs<kCap>(p, sv32, nl, pr, fac);
         if (need_mask) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            if ((unsigned)(qi - qlo) > qspan) pc[c] = pr[32 * g + c] = 0.f;
+          for (int c = 0; c < 16; ++c) {
+            float a, b;
+            f2_unpack(pr[c], a, b);
+            if ((unsigned)(qi - qlo) > qspan) a = 0.f;
             if (++qi == s.q_len) qi = 0;
+            if ((unsigned)(qi - qlo) > qspan) b = 0.f;
+            if (++qi == s.q_len) qi = 0;
+            pr[c] = f2_pack(a, b);
           }
         }
         uint32_t pk[16];
 #pragma unroll
-        for (int c = 0; c < 16; ++c) pk[c] = pack_bf16(pc[2 * c], pc[2 * c + 1]);
-        // Columns [16 g, 16 g + 16) of this half: read already (g = 0: scores
-        // 0..31 of the half; g = 1: still within them).
+        for (int c = 0; c < 16; ++c) {
+          pk[c] = pack_bf16_f2(pr[c]);
+          keep[16 * g + c] = kCap ? f2_mul(pr[c], fac[c]) : pr[c];
+        }
         tmem_st16(s_tm + 16 * g, pk);
-      }
+      };
+      tmem_ld_wait();
+      tmem_ld32(s_tm + 32, b1);
+      probs(b0, 0);
+      tmem_ld_wait();  // the second half is read before the first part is handed over
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_half);
+      probs(b1, 1);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full);
 
+      f2 dl[16];
+      bwd_load32(st + 128, dl);
       ok = __all_sync(0xffffffffu, mbar_wait(dp_full, j & 1, kStatusTimeoutSoftmax));
       if (!ok) break;
       tc_fence_after();
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        uint32_t dv32[32];
-        tmem_ld32(dp_tm + 32 * g, dv32);
-        float dl[32];
-#pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(st + 128 + 32 * g + c);
-          dl[c] = f.x;
-          dl[c + 1] = f.y;
-          dl[c + 2] = f.z;
-          dl[c + 3] = f.w;
-        }
-        tmem_ld_wait();
-        uint32_t pk[16];
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const float p0 = pr[32 * g + 2 * c], p1 = pr[32 * g + 2 * c + 1];
-          const f2 d = f2_mul(f2_pack(p0, p1),
-                              f2_sub(f2_pack(__uint_as_float(dv32[2 * c]), __uint_as_float(dv32[2 * c + 1])),
-                                     f2_pack(dl[2 * c], dl[2 * c + 1])));
-          float a, b;
-          f2_unpack(d, a, b);
-          if (need_mask) {  // a hidden score is an exact zero whatever dP is
-            a = p0 == 0.f ? 0.f : a;
-            b = p1 == 0.f ? 0.f : b;
-          }
-          pk[c] = pack_bf16(a, b);
-        }
-        tmem_st16(dp_tm + 16 * g, pk);
-      }
+      uint32_t pk[16];
+      tmem_ld32(dp_tm, b0);
+      tmem_ld32(dp_tm + 32, b1);
+      tmem_ld_wait();
+      bwd_ds(keep, b0, dl, need_mask, pk);
+      tmem_st16(dp_tm, pk);
+      bwd_load32(st + 160, dl);
+      bwd_ds(keep + 16, b1, dl, need_mask, pk);
+      tmem_st16(dp_tm + 16, pk);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -488,7 +543,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
   uint64_t* o_done = bars + 15;
   uint32_t* tmem_slot = (uint32_t*)(bars + C::kNumBars);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
     for (int i = 0; i < 3; ++i) {
@@ -557,39 +612,62 @@ __global__ void __launch_bounds__(kBwThreads, 1)
         mbar_wait(&v_full[j & 1], (j / 2) & 1, kStatusTimeoutProducer);
     }
   } else if (warp == 1) {
-    if (lane == 0 && n > 0) {
+    // The whole warp walks the loop, lane 0 issues (see mma_bf16_ss_warp).
+    if (n > 0) {
+      const uint32_t leader = lane == 0;
       const int d_pad = (s.head_dim + 15) / 16 * 16, ksteps = d_pad / 16;
       const uint32_t idesc_s = idesc_bf16_f32(128, 128, 0);
       const uint32_t idesc_o = idesc_bf16_f32(128, d_pad, 1);
-      const uint32_t qa = smem_u32(sq), da = smem_u32(sdo), ka = smem_u32(sk), va = smem_u32(sv);
-      constexpr uint32_t code = kStatusTimeoutMma;
+      const uint64_t qd = bwd_desc_k(smem_u32(sq)), dd = bwd_desc_k(smem_u32(sdo));
+      const uint64_t kk = bwd_desc_k(smem_u32(sk)), kn = bwd_desc_n<DCH>(smem_u32(sk));
+      const uint64_t vk = bwd_desc_k(smem_u32(sv));
+      constexpr uint32_t kTile = C::kTileBytes >> 4;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, kStatusTimeoutMma)) != 0;
+      };
+      auto wait_k = [&](int j) { return wait(&k_full[j % 3], (j / 3) & 1); };
+      auto wait_v = [&](int j) { return wait(&v_full[j & 1], (j / 2) & 1); };
       auto issue_s = [&](int j) {
-        if (!mbar_wait(&k_full[j % 3], (j / 3) & 1, code)) return false;
-        tc_fence_after();
-        bwd_issue_ss<DCH>(tmem + 128 * (j & 1), qa, ka + j % 3 * C::kTileBytes, idesc_s, ksteps);
-        mma_commit(&s_full[j & 1]);
-        return true;
+        bwd_issue_ss<DCH>(leader, tmem + 128 * (j & 1), qd, kk + j % 3 * kTile, idesc_s, ksteps);
+        mma_commit_warp(leader, &s_full[j & 1]);
       };
       auto issue_dp = [&](int j) {
-        if (!mbar_wait(&v_full[j & 1], (j / 2) & 1, code)) return false;
-        tc_fence_after();
-        bwd_issue_ss<DCH>(tmem + 256, da, va + (j & 1) * C::kTileBytes, idesc_s, ksteps);
-        mma_commit(dp_full);
-        mma_commit(&v_empty[j & 1]);
-        return true;
+        bwd_issue_ss<DCH>(leader, tmem + 256, dd, vk + (j & 1) * kTile, idesc_s, ksteps);
+        mma_commit_warp(leader, dp_full);
+        mma_commit_warp(leader, &v_empty[j & 1]);
       };
-      bool ok = mbar_wait(q_full, 0, code) && issue_s(0) && issue_dp(0) && (n < 2 || issue_s(1));
-      for (int j = 0; j < n && ok; ++j) {
-        // dS_j written: dP_j and S_j have been read.
-        if (!(ok = mbar_wait(ds_full, j & 1, code))) break;
-        if (j + 1 < n && !(ok = issue_dp(j + 1))) break;
+      bool ok = wait(q_full, 0) && wait_k(0);
+      if (ok) {
         tc_fence_after();
-        bwd_issue_ts<DCH>(tmem + 384, tmem + 128 * (j & 1), ka + j % 3 * C::kTileBytes, idesc_o, j == 0);
-        mma_commit(&k_empty[j % 3]);
-        if (j + 2 < n && !(ok = issue_s(j + 2))) break;
+        issue_s(0);
+        ok = wait_v(0);
       }
-      mma_commit(o_done);
-      mbar_wait(o_done, 0, code);
+      if (ok) {
+        tc_fence_after();
+        issue_dp(0);
+        ok = n < 2 || wait_k(1);
+      }
+      if (ok && n > 1) {
+        tc_fence_after();
+        issue_s(1);
+      }
+      for (int j = 0; j < n && ok; ++j) {
+        // V of the next turn is waited for ahead of it.
+        if (j + 1 < n && !(ok = wait_v(j + 1))) break;
+        // dS_j written: dP_j and S_j have been read.
+        if (!(ok = wait(ds_full, j & 1))) break;
+        tc_fence_after();
+        if (j + 1 < n) issue_dp(j + 1);
+        bwd_issue_ts(leader, tmem + 384, tmem + 128 * (j & 1), kn + j % 3 * kTile, idesc_o, j == 0, 0, 4);
+        mma_commit_warp(leader, &k_empty[j % 3]);
+        if (j + 2 < n) {
+          if (!(ok = wait_k(j + 2))) break;
+          tc_fence_after();
+          issue_s(j + 2);
+        }
+      }
+      mma_commit_warp(leader, o_done);
+      wait(o_done, 0);
     }
   } else if (warp >= 4) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kBwRegsHigh));
@@ -597,7 +675,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
     const int r = quarter * 32 + lane;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     const float* st = p.stats + ((long long)run * s.tiles + t) * 256;
-    const float lse = st[r], delta = st[128 + r];
+    const float nlse = st[r], delta = st[128 + r];
     int lo = 0, hi = -1;
     if (r < nr) {
       const int qpos = s.kv_len - s.q_len + (r0 + r) % s.q_len;
@@ -612,49 +690,49 @@ __global__ void __launch_bounds__(kBwThreads, 1)
       const int vlo = chi >= clo ? clo : 128;
       const unsigned vspan = chi >= clo ? (unsigned)(chi - clo) : 0u;
       const uint32_t s_tm = tmem + lane_base + 128 * (j & 1) + 64 * h;
-      float pr[64];
+      f2 keep[32];
       ok = __all_sync(0xffffffffu, mbar_wait(&s_full[j & 1], (j / 2) & 1, kStatusTimeoutSoftmax));
       if (!ok) break;
       tc_fence_after();
+      uint32_t b0[32], b1[32];
+      f2 row[16];
+      auto probs = [&](const uint32_t(&sv32)[32], int g) {
+        f2 pr[16], fac[16];
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        uint32_t sv32[32];
-        float l32[32], pc[32];
-        tmem_ld32(s_tm + 32 * g, sv32);
-#pragma unroll
-        for (int c = 0; c < 32; ++c) l32[c] = lse;
-        tmem_ld_wait();
-        bwd_probs<kCap>(p, sv32, l32, pc, &pr[32 * g]);
+        for (int c = 0; c < 16; ++c) row[c] = f2_pack(nlse, nlse);
+        bwd_probs<kCap>(p, sv32, row, pr, fac);
         if (need_mask) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if ((unsigned)(64 * h + 32 * g + c - vlo) > vspan) pr[32 * g + c] = 0.f;
+          for (int c = 0; c < 16; ++c) {
+            const int col = 64 * h + 32 * g + 2 * c;
+            float a, b;
+            f2_unpack(pr[c], a, b);
+            pr[c] = f2_pack((unsigned)(col - vlo) > vspan ? 0.f : a,
+                            (unsigned)(col + 1 - vlo) > vspan ? 0.f : b);
+          }
         }
-      }
+#pragma unroll
+        for (int c = 0; c < 16; ++c) keep[16 * g + c] = kCap ? f2_mul(pr[c], fac[c]) : pr[c];
+      };
+      tmem_ld32(s_tm, b0);
+      tmem_ld_wait();
+      tmem_ld32(s_tm + 32, b1);
+      probs(b0, 0);
+      tmem_ld_wait();
+      probs(b1, 1);
       ok = __all_sync(0xffffffffu, mbar_wait(dp_full, j & 1, kStatusTimeoutSoftmax));
       if (!ok) break;
       tc_fence_after();
-      const f2 dl = f2_pack(delta, delta);
+      uint32_t pk[16];
+      tmem_ld32(tmem + lane_base + 256 + 64 * h, b0);
+      tmem_ld32(tmem + lane_base + 288 + 64 * h, b1);
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        uint32_t dv32[32], pk[16];
-        tmem_ld32(tmem + lane_base + 256 + 64 * h + 32 * g, dv32);
-        tmem_ld_wait();
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const float p0 = pr[32 * g + 2 * c], p1 = pr[32 * g + 2 * c + 1];
-          const f2 d = f2_mul(f2_pack(p0, p1),
-                              f2_sub(f2_pack(__uint_as_float(dv32[2 * c]), __uint_as_float(dv32[2 * c + 1])), dl));
-          float a, b;
-          f2_unpack(d, a, b);
-          if (need_mask) {
-            a = p0 == 0.f ? 0.f : a;
-            b = p1 == 0.f ? 0.f : b;
-          }
-          pk[c] = pack_bf16(a, b);
-        }
-        tmem_st16(s_tm + 16 * g, pk);
-      }
+      for (int c = 0; c < 16; ++c) row[c] = f2_pack(delta, delta);
+      tmem_ld_wait();
+      bwd_ds(keep, b0, row, need_mask, pk);
+      tmem_st16(s_tm, pk);
+      bwd_ds(keep + 16, b1, row, need_mask, pk);
+      tmem_st16(s_tm + 16, pk);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
