@@ -1,11 +1,13 @@
 // backward_sm100.cuh -- the backward pass on the 5th-generation tensor cores
 // (head_dim up to 128); backward.cuh has the formulas and the row layout.
 //
-// Two kernels with the same frame, one CTA of 12 warps per tile of 128 and
-// per SM:
+// Two kernels with the same frame, one CTA of 12 warps per SM that walks work
+// items (a key tile, or a row tile, of 128) in rounds of the grid; barriers,
+// TMEM and the rings live across items, so the next item's loads and first
+// products run under the current one's last steps and its stores:
 //   warp 0      TMA loader (and the statistics' bulk copies);
-//   warp 1      TMEM allocator; its lane 0 issues every tcgen05.mma;
-//   warps 2-3   idle (they complete warpgroup 0 for the register split);
+//   warp 1      TMEM allocator; warps 1 and 2 issue the tcgen05.mma (a lane each);
+//   warp 3      idle (it completes warpgroup 0 for the register split);
 //   warps 4-11  elementwise work: warpgroup h takes columns [64 h, 64 h + 64)
 //               of the 128 x 128 tiles, a thread one lane (row) of them.
 //
@@ -54,7 +56,7 @@ struct BwdCfg {
   static constexpr int kRing2 = kRing3 + 3 * kTileBytes;
   static constexpr int kStats = kRing2 + 2 * kTileBytes;  // two slots of 256 floats
   static constexpr int kBars = kStats + 2 * 1024;
-  static constexpr int kNumBars = 24;
+  static constexpr int kNumBars = 26;
   static constexpr int kSmemBytes = kBars + kNumBars * 8 + 16;
 };
 
@@ -160,21 +162,19 @@ __device__ __forceinline__ void bwd_load32(const float* src, f2 (&v)[16]) {
   }
 }
 
-// One 128 x 64-column piece of TMEM (this warp's 32 lanes) scaled, rounded to
-// bf16 and stored through a swizzled 32-row box and TMA; rows and columns
-// outside the tensor are not written.
-__device__ __forceinline__ void bwd_store_box(const CUtensorMap* map, uint8_t* stage, uint32_t tm,
-                                              int c0, int cols, int row, int outer, float scale,
-                                              bool zero, int lane) {
-  if (lane == 0) bulk_wait_read();
-  __syncwarp();
-  for (int c1 = 0; c1 < cols; c1 += 16) {
+// This thread's row of an fp32 accumulator in TMEM, columns [c0, c1) (whole
+// 16s; `cols` of them exist), scaled and rounded to bf16.  Stored from
+// registers, 32 bytes at a time: shared memory has no room to stage a tile
+// next to the rings, and the next item's loads are already under way.
+__device__ __forceinline__ void bwd_store_row(__nv_bfloat16* dst, uint32_t tm, int c0, int c1,
+                                              int cols, float scale, bool zero, bool live) {
+  for (int c = c0; c < c1; c += 16) {
     uint32_t v[16];
     if (zero) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) v[e] = 0u;
     } else {
-      tmem_ld16(tm + c0 + c1, v);
+      tmem_ld16(tm + c, v);
       tmem_ld_wait();
     }
 #pragma unroll
@@ -184,16 +184,18 @@ __device__ __forceinline__ void bwd_store_box(const CUtensorMap* map, uint8_t* s
       for (int e = 0; e < 4; ++e)
         w[e] = pack_bf16(__uint_as_float(v[8 * g + 2 * e]) * scale,
                          __uint_as_float(v[8 * g + 2 * e + 1]) * scale);
-      *reinterpret_cast<uint4*>(stage + sw128(lane, (c1 >> 3) + g)) =
-          make_uint4(w[0], w[1], w[2], w[3]);
+      if (live && c + 8 * g < cols)
+        *reinterpret_cast<uint4*>(dst + c + 8 * g) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) {
-    tma_store_3d(map, stage, c0, row, outer);
-    bulk_commit();
-  }
+}
+
+// The k-th item of this CTA: items go out in rounds of the grid, every other
+// round backwards when they are sorted heavy first, so that no CTA takes the
+// heaviest of every round.
+__device__ __forceinline__ int bwd_item(const BwdShape& s, int k) {
+  const int G = (int)gridDim.x, c = (int)blockIdx.x;
+  return k * G + (((s.causal || s.window > 0) && (k & 1)) ? G - 1 - c : c);
 }
 
 // The products, 8 K-steps of 16 unless K is head_dim.  Shared memory lies
@@ -214,8 +216,9 @@ __device__ __forceinline__ void bwd_issue_ss(uint32_t leader, uint32_t d, uint64
 // A (128 x 128 bf16) from TMEM: columns 0..63 of the tile at a, 64..127 at
 // a + 64; B (128 x N) from shared memory, N contiguous.  K-steps [k0, k1) of
 // both halves.
+template <int k0, int k1>
 __device__ __forceinline__ void bwd_issue_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t bd,
-                                             uint32_t idesc, bool first, int k0, int k1) {
+                                             uint32_t idesc, bool first) {
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -236,7 +239,6 @@ template <int DCH, bool kCap>
 __global__ void __launch_bounds__(kBwThreads, 1)
     bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                    const __grid_constant__ CUtensorMap tm_dk, const __grid_constant__ CUtensorMap tm_dv,
                     const BwdParams p) {
   using C = BwdCfg<DCH>;
   const BwdShape& s = p.sh;
@@ -247,40 +249,49 @@ __global__ void __launch_bounds__(kBwThreads, 1)
   uint8_t* sdo = smem + C::kRing2;
   float* stats = (float*)(smem + C::kStats);
   uint64_t* bars = (uint64_t*)(smem + C::kBars);
-  uint64_t* kv_full = bars;
+  uint64_t* k_full = bars;
   uint64_t* q_full = bars + 1;    // [3]
   uint64_t* q_empty = bars + 4;   // [3]
   uint64_t* do_full = bars + 7;   // [2]
   uint64_t* do_empty = bars + 9;  // [2]
   uint64_t* st_full = bars + 11;  // [2]
   uint64_t* st_empty = bars + 13; // [2]
-  uint64_t* s_full = bars + 15;
-  uint64_t* dp_full = bars + 16;
-  uint64_t* p_full = bars + 17;
-  uint64_t* ds_full = bars + 18;
-  uint64_t* o_done = bars + 19;
-  uint64_t* p_half = bars + 20;
+  uint64_t* s_full = bars + 15;   // [2], by tile: two roles wait for it, a step apart
+  uint64_t* dp_full = bars + 17;
+  uint64_t* p_half = bars + 18;
+  uint64_t* p_full = bars + 19;
+  uint64_t* ds_full = bars + 20;
+  uint64_t* o_done = bars + 21;
+  uint64_t* k_empty = bars + 22;
+  uint64_t* v_full = bars + 23;
+  uint64_t* v_empty = bars + 24;
+  uint64_t* drain = bars + 25;
   uint32_t* tmem_slot = (uint32_t*)(bars + C::kNumBars);
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    mbar_init(kv_full, 1);
+    mbar_init(k_full, 1);
+    mbar_init(k_empty, 1);
+    mbar_init(drain, 2);
+    mbar_init(v_full, 1);
+    mbar_init(v_empty, 1);
     for (int i = 0; i < 3; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&do_full[i], 1);
-      mbar_init(&do_empty[i], 1);
+      mbar_init(&do_empty[i], 2);  // both issuers
       mbar_init(&st_full[i], 1);
       mbar_init(&st_empty[i], 8);
     }
-    mbar_init(s_full, 1);
-    mbar_init(dp_full, 1);
+    mbar_init(&s_full[0], 1);
+    mbar_init(&s_full[1], 1);
     mbar_init(p_half, 8);
+    mbar_init(dp_full, 1);
     mbar_init(p_full, 8);
     mbar_init(ds_full, 8);
-    mbar_init(o_done, 1);
+    mbar_init(o_done, 2);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -292,121 +303,165 @@ __global__ void __launch_bounds__(kBwThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  // Key tiles in ascending order: under a causal mask the first ones have the
-  // most rows, so the light ones fill the last wave.
-  const int unit = (int)(blockIdx.x % (unsigned)s.units);
-  const int k0 = (int)(blockIdx.x / (unsigned)s.units) * 128;
-  int first, count;
-  bwd_row_tiles(s, k0, min(k0 + 127, s.kv_len - 1), 128, first, count);
-  const int n = count * s.runs_per_unit;
-  const int run0 = unit * s.runs_per_unit;
+  // Item i: unit i % units, key tile i / units, in ascending order: under a
+  // causal mask the first ones have the most rows.
+  const int units = (int)s.units;
+  const int items = units * ((s.kv_len + 127) / 128);
+  struct Item {
+    int unit, k0, first, count, n;
+  };
+  auto item_at = [&](int i) {
+    Item t;
+    t.unit = i % units;
+    t.k0 = i / units * 128;
+    bwd_row_tiles(s, t.k0, min(t.k0 + 127, s.kv_len - 1), 128, t.first, t.count);
+    t.n = t.count * s.runs_per_unit;
+    return t;
+  };
 
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBwRegsLow));
   if (warp == 0) {
-    if (lane == 0 && n > 0) {
+    if (lane == 0) {
       tma_prefetch_map(&tm_q);
       tma_prefetch_map(&tm_do);
-      mbar_arrive_expect_tx(kv_full, 2 * C::kTileBytes);
-      for (int c = 0; c < DCH; ++c)
-        tma_load_3d(sk + c * C::kBoxBytes, &tm_k, kv_full, c * 64, k0, unit);
-      for (int c = 0; c < DCH; ++c)
-        tma_load_3d(sv + c * C::kBoxBytes, &tm_v, kv_full, c * 64, k0, unit);
+      tma_prefetch_map(&tm_k);
+      tma_prefetch_map(&tm_v);
+      constexpr uint32_t code = kStatusTimeoutProducer;
+      auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int row, int outer) {
+        mbar_arrive_expect_tx(bar, C::kTileBytes);
+        for (int c = 0; c < DCH; ++c)
+          tma_load_3d(dst + c * C::kBoxBytes, map, bar, c * 64, row, outer);
+      };
+      int J = 0, busy = 0;         // row tiles and items so far
       int jq = 0, jd = 0, js = 0;  // loads issued
-      int run = run0, t = first;
-      for (int j = 0; j < n; ++j) {
-        if (j >= 3 && !mbar_wait(&q_empty[j % 3], (j / 3 - 1) & 1, kStatusTimeoutProducer)) break;
-        mbar_arrive_expect_tx(&q_full[j % 3], C::kTileBytes);
-        for (int c = 0; c < DCH; ++c)
-          tma_load_3d(sq + (j % 3) * C::kTileBytes + c * C::kBoxBytes, &tm_q, &q_full[j % 3], c * 64,
-                      t * 128, run);
-        ++jq;
-        if (j >= 2 && !mbar_wait(&do_empty[j & 1], (j / 2 - 1) & 1, kStatusTimeoutProducer)) break;
-        mbar_arrive_expect_tx(&do_full[j & 1], C::kTileBytes);
-        for (int c = 0; c < DCH; ++c)
-          tma_load_3d(sdo + (j & 1) * C::kTileBytes + c * C::kBoxBytes, &tm_do, &do_full[j & 1],
-                      c * 64, t * 128, run);
-        ++jd;
-        if (j >= 2 && !mbar_wait(&st_empty[j & 1], (j / 2 - 1) & 1, kStatusTimeoutProducer)) break;
-        mbar_arrive_expect_tx(&st_full[j & 1], 1024);
-        bulk_load(stats + (j & 1) * 256, p.stats + ((long long)run * s.tiles + t) * 256, 1024,
-                  &st_full[j & 1]);
-        ++js;
-        if (++t == first + count) {
-          t = first;
-          ++run;
+      int nk = 0, nv = 0;
+      bool ok = true;
+      for (int kk = 0, i = bwd_item(s, 0); i < items && ok; i = bwd_item(s, ++kk)) {
+        const Item it = item_at(i);
+        if (it.n == 0) continue;
+        if (busy > 0 && !(ok = mbar_wait(k_empty, (busy - 1) & 1, code))) break;
+        load(sk, &tm_k, k_full, it.k0, it.unit);
+        ++nk;
+        int run = it.unit * s.runs_per_unit, t = it.first;
+        for (int j = 0; j < it.n; ++j, ++J) {
+          const int q3 = J % 3, d2 = J & 1;
+          if (J >= 3 && !(ok = mbar_wait(&q_empty[q3], (J / 3 - 1) & 1, code))) break;
+          load(sq + q3 * C::kTileBytes, &tm_q, &q_full[q3], t * 128, run);
+          ++jq;
+          if (j == 0) {
+            if (busy > 0 && !(ok = mbar_wait(v_empty, (busy - 1) & 1, code))) break;
+            load(sv, &tm_v, v_full, it.k0, it.unit);
+            ++nv;
+          }
+          if (J >= 2 && !(ok = mbar_wait(&do_empty[d2], (J / 2 - 1) & 1, code))) break;
+          load(sdo + d2 * C::kTileBytes, &tm_do, &do_full[d2], t * 128, run);
+          ++jd;
+          if (J >= 2 && !(ok = mbar_wait(&st_empty[d2], (J / 2 - 1) & 1, code))) break;
+          mbar_arrive_expect_tx(&st_full[d2], 1024);
+          bulk_load(stats + d2 * 256, p.stats + ((long long)run * s.tiles + t) * 256, 1024, &st_full[d2]);
+          ++js;
+          if (++t == it.first + it.count) {
+            t = it.first;
+            ++run;
+          }
         }
+        ++busy;
       }
       // Never leave with copies in flight.
-      mbar_wait(kv_full, 0, kStatusTimeoutProducer);
-      for (int j = max(0, jq - 3); j < jq; ++j)
-        mbar_wait(&q_full[j % 3], (j / 3) & 1, kStatusTimeoutProducer);
-      for (int j = max(0, jd - 2); j < jd; ++j)
-        mbar_wait(&do_full[j & 1], (j / 2) & 1, kStatusTimeoutProducer);
-      for (int j = max(0, js - 2); j < js; ++j)
-        mbar_wait(&st_full[j & 1], (j / 2) & 1, kStatusTimeoutProducer);
+      if (nk > 0) mbar_wait(k_full, (nk - 1) & 1, code);
+      if (nv > 0) mbar_wait(v_full, (nv - 1) & 1, code);
+      for (int j = max(0, jq - 3); j < jq; ++j) mbar_wait(&q_full[j % 3], (j / 3) & 1, code);
+      for (int j = max(0, jd - 2); j < jd; ++j) mbar_wait(&do_full[j & 1], (j / 2) & 1, code);
+      for (int j = max(0, js - 2); j < js; ++j) mbar_wait(&st_full[j & 1], (j / 2) & 1, code);
     }
-  } else if (warp == 1) {
-    // The whole warp walks the loop, lane 0 issues (see mma_bf16_ss_warp).
-    if (n > 0) {
-      const uint32_t leader = lane == 0;
-      const int d_pad = (s.head_dim + 15) / 16 * 16, ksteps = d_pad / 16;
-      const uint32_t idesc_s = idesc_bf16_f32(128, 128, 0);
-      const uint32_t idesc_o = idesc_bf16_f32(128, d_pad, 1);
-      const uint64_t kd = bwd_desc_k(smem_u32(sk)), vd = bwd_desc_k(smem_u32(sv));
-      const uint64_t qk = bwd_desc_k(smem_u32(sq)), qn = bwd_desc_n<DCH>(smem_u32(sq));
-      const uint64_t dk = bwd_desc_k(smem_u32(sdo)), dn = bwd_desc_n<DCH>(smem_u32(sdo));
-      constexpr uint32_t kTile = C::kTileBytes >> 4;  // a slot, in descriptor units
-      // Uniform over the warp, so that it stays converged.
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity, kStatusTimeoutMma)) != 0;
-      };
-      bool ok = wait(kv_full, 0) && wait(&q_full[0], 0);
-      if (ok) {
+  } else if (warp == 1 || warp == 2) {
+    // Two issuers: warp 1 the products S^T and dV, warp 2 dP^T and dK.  While
+    // one waits for its next operand, the other one's products fill the
+    // tensor core; each writes its own TMEM columns, in its own order.  The
+    // whole warp walks the loop, lane 0 issues (see mma_bf16_ss_warp).
+    const uint32_t leader = lane == 0;
+    const int d_pad = (s.head_dim + 15) / 16 * 16, ksteps = d_pad / 16;
+    const uint32_t idesc_s = idesc_bf16_f32(128, 128, 0);
+    const uint32_t idesc_o = idesc_bf16_f32(128, d_pad, 1);
+    const uint64_t kd = bwd_desc_k(smem_u32(sk)), vd = bwd_desc_k(smem_u32(sv));
+    const uint64_t qk = bwd_desc_k(smem_u32(sq)), qn = bwd_desc_n<DCH>(smem_u32(sq));
+    const uint64_t dk = bwd_desc_k(smem_u32(sdo)), dn = bwd_desc_n<DCH>(smem_u32(sdo));
+    constexpr uint32_t kTile = C::kTileBytes >> 4;  // a slot, in descriptor units
+    // Waits are uniform over the warp, so that it stays converged.
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, kStatusTimeoutMma)) != 0;
+    };
+    int J = 0, busy = 0;
+    int sq_j = 0, sq_n = 1;  // Q slots of row tiles J and J + 1
+    bool ok = true;
+    for (int kk = 0, i = bwd_item(s, 0); i < items && ok; i = bwd_item(s, ++kk)) {
+      const int n = item_at(i).n;
+      if (n == 0) continue;
+      if (warp == 1) {
+        if (!(ok = wait(k_full, busy & 1) && wait(&q_full[sq_j], (J / 3) & 1))) break;
         tc_fence_after();
-        bwd_issue_ss<DCH>(leader, tmem, kd, qk, idesc_s, ksteps);
-        mma_commit_warp(leader, s_full);
-      }
-      int sq_j = 0, sq_n = 1;  // Q slots of tiles j and j + 1
-      ok = ok && wait(&do_full[0], 0);
-      for (int j = 0; j < n && ok; ++j) {
-        const uint32_t doj = (j & 1) * kTile;
-        const bool more = j + 1 < n;
-        tc_fence_after();
-        bwd_issue_ss<DCH>(leader, tmem + 128, vd, dk + doj, idesc_s, ksteps);
-        mma_commit_warp(leader, dp_full);
-        // dV in two parts: rows 0..31 and 64..95 of the tile first.
-        if (!(ok = wait(p_half, j & 1))) break;
-        tc_fence_after();
-        bwd_issue_ts(leader, tmem + 256, tmem, dn + doj, idesc_o, j == 0, 0, 2);
-        // The next tile's operands are waited for ahead of their turn.
-        if (more && !(ok = wait(&q_full[sq_n], ((j + 1) / 3) & 1))) break;
-        if (!(ok = wait(p_full, j & 1))) break;
-        tc_fence_after();
-        bwd_issue_ts(leader, tmem + 256, tmem, dn + doj, idesc_o, false, 2, 4);
-        mma_commit_warp(leader, &do_empty[j & 1]);
-        if (more) {
-          bwd_issue_ss<DCH>(leader, tmem, kd, qk + sq_n * kTile, idesc_s, ksteps);
-          mma_commit_warp(leader, s_full);
-          if (!(ok = wait(&do_full[(j + 1) & 1], ((j + 1) / 2) & 1))) break;
+        bwd_issue_ss<DCH>(leader, tmem, kd, qk + sq_j * kTile, idesc_s, ksteps);
+        mma_commit_warp(leader, &s_full[J & 1]);
+        if (n == 1) mma_commit_warp(leader, k_empty);
+        for (int j = 0; j < n; ++j, ++J) {
+          const bool more = j + 1 < n;
+          // Loads first: they are there long before P is.
+          if (!(ok = wait(&do_full[J & 1], (J / 2) & 1))) break;
+          if (more && !(ok = wait(&q_full[sq_n], ((J + 1) / 3) & 1))) break;
+          // dV in two parts: rows 0..31 and 64..95 of the tile first, so that
+          // the next S^T waits for half a product only once P^T is complete.
+          if (!(ok = wait(p_half, J & 1))) break;
+          tc_fence_after();
+          bwd_issue_ts<0, 2>(leader, tmem + 256, tmem, dn + (J & 1) * kTile, idesc_o, j == 0);
+          if (!(ok = wait(p_full, J & 1))) break;
+          tc_fence_after();
+          bwd_issue_ts<2, 4>(leader, tmem + 256, tmem, dn + (J & 1) * kTile, idesc_o, false);
+          mma_commit_warp(leader, &do_empty[J & 1]);
+          if (more) {
+            bwd_issue_ss<DCH>(leader, tmem, kd, qk + sq_n * kTile, idesc_s, ksteps);
+            mma_commit_warp(leader, &s_full[(J + 1) & 1]);
+            if (j + 2 == n) mma_commit_warp(leader, k_empty);
+          }
+          sq_j = sq_n;
+          if (++sq_n == 3) sq_n = 0;
         }
-        if (!(ok = wait(ds_full, j & 1))) break;
-        tc_fence_after();
-        bwd_issue_ts(leader, tmem + 384, tmem + 128, qn + sq_j * kTile, idesc_o, j == 0, 0, 4);
-        mma_commit_warp(leader, &q_empty[sq_j]);
-        sq_j = sq_n;
-        if (++sq_n == 3) sq_n = 0;
+      } else {
+        if (!(ok = wait(v_full, busy & 1))) break;
+        for (int j = 0; j < n; ++j, ++J) {
+          if (!(ok = wait(&do_full[J & 1], (J / 2) & 1))) break;
+          tc_fence_after();
+          bwd_issue_ss<DCH>(leader, tmem + 128, vd, dk + (J & 1) * kTile, idesc_s, ksteps);
+          mma_commit_warp(leader, dp_full);
+          mma_commit_warp(leader, &do_empty[J & 1]);
+          if (j + 1 == n) mma_commit_warp(leader, v_empty);
+          if (!(ok = wait(&q_full[sq_j], (J / 3) & 1) && wait(ds_full, J & 1))) break;
+          // The next S^T goes first: P^T waits for it, nothing waits for dK.
+          if (j + 1 < n && !(ok = wait(&s_full[(J + 1) & 1], ((J + 1) / 2) & 1))) break;
+          tc_fence_after();
+          bwd_issue_ts<0, 4>(leader, tmem + 384, tmem + 128, qn + sq_j * kTile, idesc_o, j == 0);
+          mma_commit_warp(leader, &q_empty[sq_j]);
+          if (++sq_j == 3) sq_j = 0;
+        }
       }
-      // Every product finished before the epilogue, and before TMEM is freed.
+      if (!ok) break;
       mma_commit_warp(leader, o_done);
-      wait(o_done, 0);
+      ++busy;
     }
+    // Every product finished before TMEM is freed.
+    mma_commit_warp(leader, drain);
+    wait(drain, 0);
   } else if (warp >= 4) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kBwRegsHigh));
     const int h = (warp - 4) >> 2, quarter = warp & 3;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     const uint32_t s_tm = tmem + lane_base + 64 * h, dp_tm = s_tm + 128;
-    const int key = k0 + quarter * 32 + lane;
     const MaskSpec ms = bwd_mask(s);
+    const int d_pad = (s.head_dim + 15) / 16 * 16;
+    int J = 0, busy = 0;
+    bool ok = true;
+    for (int kk = 0, i = bwd_item(s, 0); i < items && ok; i = bwd_item(s, ++kk)) {
+    const Item it = item_at(i);
+    const int key = it.k0 + quarter * 32 + lane;
     // Queries that see this lane's key: [qlo, qlo + qspan] (none past kv_len).
     int qlo, qhi;
     bwd_query_range(s, key, key, qlo, qhi);
@@ -415,15 +470,15 @@ __global__ void __launch_bounds__(kBwThreads, 1)
       qhi = 0x7fffffff;
     }
     const unsigned qspan = (unsigned)(qhi - qlo);
-    bool ok = true;
-    int run = run0, t = first;
-    for (int j = 0; j < n; ++j) {
+    int t = it.first;
+    for (int j = 0; j < it.n; ++j, ++J) {
       const int r0 = t * 128, nr = min(128, s.run - r0);
-      const bool need_mask = bwd_need_mask(s, ms, r0, nr, k0);
+      const bool need_mask = bwd_need_mask(s, ms, r0, nr, it.k0);
+      const uint32_t par = J & 1, dpar = (J / 2) & 1;
       f2 keep[32];
-      const float* st = stats + (j & 1) * 256 + 64 * h;
-      ok = mbar_wait(&st_full[j & 1], (j / 2) & 1, kStatusTimeoutSoftmax) &&
-           mbar_wait(s_full, j & 1, kStatusTimeoutSoftmax);
+      const float* st = stats + par * 256 + 64 * h;
+      ok = mbar_wait(&st_full[par], dpar, kStatusTimeoutSoftmax) &&
+           mbar_wait(&s_full[par], dpar, kStatusTimeoutSoftmax);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
@@ -459,7 +514,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
       tmem_ld_wait();
       tmem_ld32(s_tm + 32, b1);
       probs(b0, 0);
-      tmem_ld_wait();  // the second half is read before the first part is handed over
+      tmem_ld_wait();
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -472,7 +527,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
 
       f2 dl[16];
       bwd_load32(st + 128, dl);
-      ok = __all_sync(0xffffffffu, mbar_wait(dp_full, j & 1, kStatusTimeoutSoftmax));
+      ok = __all_sync(0xffffffffu, mbar_wait(dp_full, par, kStatusTimeoutSoftmax));
       if (!ok) break;
       tc_fence_after();
       uint32_t pk[16];
@@ -489,25 +544,23 @@ __global__ void __launch_bounds__(kBwThreads, 1)
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(ds_full);
-        mbar_arrive(&st_empty[j & 1]);
+        mbar_arrive(&st_empty[par]);
       }
-      if (++t == first + count) {
-        t = first;
-        ++run;
-      }
+      if (++t == it.first + it.count) t = it.first;
     }
-    if (n > 0 && ok)
-      ok = __all_sync(0xffffffffu, mbar_wait(o_done, 0, kStatusTimeoutEpilogue));
-    if (ok) {
+    if (!ok) break;
+    if (it.n > 0) {
+      ok = __all_sync(0xffffffffu, mbar_wait(o_done, busy & 1, kStatusTimeoutEpilogue));
+      if (!ok) break;
+      ++busy;
       tc_fence_after();
-      // Warpgroup 0 stores dV, warpgroup 1 dK, through boxes in the Q ring
-      // (every load into it has been consumed).
-      uint8_t* stage = sq + (warp - 4) * 4096;
-      const int d_pad = (s.head_dim + 15) / 16 * 16;
-      for (int c0 = 0; c0 < d_pad && k0 + quarter * 32 < s.kv_len; c0 += 64)
-        bwd_store_box(h ? &tm_dk : &tm_dv, stage, tmem + lane_base + 256 + 128 * h, c0,
-                      min(64, d_pad - c0), k0 + quarter * 32, unit, h ? p.scale : 1.f, n == 0, lane);
-      if (lane == 0) bulk_wait_all();
+    }
+    // Warpgroup 0 stores dV, warpgroup 1 dK.  The next item's first products
+    // into them follow this thread's next P and dS arrivals.
+    if (it.k0 + quarter * 32 < s.kv_len)
+      bwd_store_row((h ? p.dk : p.dv) + ((long long)it.unit * s.kv_len + key) * s.head_dim,
+                    tmem + lane_base + 256 + 128 * h, 0, d_pad, s.head_dim, h ? p.scale : 1.f,
+                    it.n == 0, key < s.kv_len);
     }
   }
   tc_fence_before();
@@ -523,7 +576,7 @@ template <int DCH, bool kCap>
 __global__ void __launch_bounds__(kBwThreads, 1)
     bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                   const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                  const __grid_constant__ CUtensorMap tm_dq, const BwdParams p) {
+                  const BwdParams p) {
   using C = BwdCfg<DCH>;
   const BwdShape& s = p.sh;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -539,8 +592,14 @@ __global__ void __launch_bounds__(kBwThreads, 1)
   uint64_t* v_empty = bars + 9;  // [2]
   uint64_t* s_full = bars + 11;  // [2]
   uint64_t* dp_full = bars + 13;
+  // [2], by tile: with one barrier, the issuer of dQ could find the phase
+  // after its own complete as well and take it for none.
   uint64_t* ds_full = bars + 14;
-  uint64_t* o_done = bars + 15;
+  uint64_t* o_done = bars + 16;
+  uint64_t* q_empty = bars + 17;
+  uint64_t* do_full = bars + 18;
+  uint64_t* do_empty = bars + 19;
+  uint64_t* drain = bars + 20;
   uint32_t* tmem_slot = (uint32_t*)(bars + C::kNumBars);
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -554,10 +613,14 @@ __global__ void __launch_bounds__(kBwThreads, 1)
       mbar_init(&v_full[i], 1);
       mbar_init(&v_empty[i], 1);
       mbar_init(&s_full[i], 1);
+      mbar_init(&ds_full[i], 8);
     }
     mbar_init(dp_full, 1);
-    mbar_init(ds_full, 8);
     mbar_init(o_done, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(do_full, 1);
+    mbar_init(do_empty, 1);
+    mbar_init(drain, 2);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -569,129 +632,160 @@ __global__ void __launch_bounds__(kBwThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  // Row tiles in descending order: under a causal mask the last ones have the
-  // most keys.  Runs of one kv head follow each other and share K and V in L2.
-  const int run = (int)(blockIdx.x % (unsigned)s.runs);
-  const int t = s.tiles - 1 - (int)(blockIdx.x / (unsigned)s.runs);
-  const int r0 = t * 128, nr = min(128, s.run - r0);
-  const int unit = run / s.runs_per_unit;
+  // Item i: run i % runs, row tile from the last down: under a causal mask
+  // the last ones have the most keys.  Runs of one kv head follow each other
+  // and share K and V in L2.
   const MaskSpec ms = bwd_mask(s);
-  const KeyRange kr = key_range(ms, r0, nr, 128);
-  const int n = kr.t_count;
+  const int runs = (int)s.runs, items = runs * s.tiles;
+  struct Item {
+    int run, unit, r0, nr, tile;
+    KeyRange kr;
+  };
+  auto item_at = [&](int i) {
+    Item t;
+    t.run = i % runs;
+    t.tile = s.tiles - 1 - i / runs;
+    t.r0 = t.tile * 128;
+    t.nr = min(128, s.run - t.r0);
+    t.unit = t.run / s.runs_per_unit;
+    t.kr = key_range(ms, t.r0, t.nr, 128);
+    return t;
+  };
 
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBwRegsLow));
   if (warp == 0) {
-    if (lane == 0 && n > 0) {
+    if (lane == 0) {
+      tma_prefetch_map(&tm_q);
+      tma_prefetch_map(&tm_do);
       tma_prefetch_map(&tm_k);
       tma_prefetch_map(&tm_v);
-      mbar_arrive_expect_tx(q_full, 2 * C::kTileBytes);
-      for (int c = 0; c < DCH; ++c)
-        tma_load_3d(sq + c * C::kBoxBytes, &tm_q, q_full, c * 64, r0, run);
-      for (int c = 0; c < DCH; ++c)
-        tma_load_3d(sdo + c * C::kBoxBytes, &tm_do, q_full, c * 64, r0, run);
-      int jk = 0, jv = 0;
-      for (int j = 0; j < n; ++j) {
-        const int key0 = (kr.t_first + j) * 128;
-        if (j >= 3 && !mbar_wait(&k_empty[j % 3], (j / 3 - 1) & 1, kStatusTimeoutProducer)) break;
-        mbar_arrive_expect_tx(&k_full[j % 3], C::kTileBytes);
+      constexpr uint32_t code = kStatusTimeoutProducer;
+      auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int row, int outer) {
+        mbar_arrive_expect_tx(bar, C::kTileBytes);
         for (int c = 0; c < DCH; ++c)
-          tma_load_3d(sk + (j % 3) * C::kTileBytes + c * C::kBoxBytes, &tm_k, &k_full[j % 3], c * 64,
-                      key0, unit);
-        ++jk;
-        if (j >= 2 && !mbar_wait(&v_empty[j & 1], (j / 2 - 1) & 1, kStatusTimeoutProducer)) break;
-        mbar_arrive_expect_tx(&v_full[j & 1], C::kTileBytes);
-        for (int c = 0; c < DCH; ++c)
-          tma_load_3d(sv + (j & 1) * C::kTileBytes + c * C::kBoxBytes, &tm_v, &v_full[j & 1], c * 64,
-                      key0, unit);
-        ++jv;
-      }
-      mbar_wait(q_full, 0, kStatusTimeoutProducer);
-      for (int j = max(0, jk - 3); j < jk; ++j)
-        mbar_wait(&k_full[j % 3], (j / 3) & 1, kStatusTimeoutProducer);
-      for (int j = max(0, jv - 2); j < jv; ++j)
-        mbar_wait(&v_full[j & 1], (j / 2) & 1, kStatusTimeoutProducer);
-    }
-  } else if (warp == 1) {
-    // The whole warp walks the loop, lane 0 issues (see mma_bf16_ss_warp).
-    if (n > 0) {
-      const uint32_t leader = lane == 0;
-      const int d_pad = (s.head_dim + 15) / 16 * 16, ksteps = d_pad / 16;
-      const uint32_t idesc_s = idesc_bf16_f32(128, 128, 0);
-      const uint32_t idesc_o = idesc_bf16_f32(128, d_pad, 1);
-      const uint64_t qd = bwd_desc_k(smem_u32(sq)), dd = bwd_desc_k(smem_u32(sdo));
-      const uint64_t kk = bwd_desc_k(smem_u32(sk)), kn = bwd_desc_n<DCH>(smem_u32(sk));
-      const uint64_t vk = bwd_desc_k(smem_u32(sv));
-      constexpr uint32_t kTile = C::kTileBytes >> 4;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity, kStatusTimeoutMma)) != 0;
+          tma_load_3d(dst + c * C::kBoxBytes, map, bar, c * 64, row, outer);
       };
-      auto wait_k = [&](int j) { return wait(&k_full[j % 3], (j / 3) & 1); };
-      auto wait_v = [&](int j) { return wait(&v_full[j & 1], (j / 2) & 1); };
-      auto issue_s = [&](int j) {
-        bwd_issue_ss<DCH>(leader, tmem + 128 * (j & 1), qd, kk + j % 3 * kTile, idesc_s, ksteps);
-        mma_commit_warp(leader, &s_full[j & 1]);
-      };
-      auto issue_dp = [&](int j) {
-        bwd_issue_ss<DCH>(leader, tmem + 256, dd, vk + (j & 1) * kTile, idesc_s, ksteps);
-        mma_commit_warp(leader, dp_full);
-        mma_commit_warp(leader, &v_empty[j & 1]);
-      };
-      bool ok = wait(q_full, 0) && wait_k(0);
-      if (ok) {
-        tc_fence_after();
-        issue_s(0);
-        ok = wait_v(0);
-      }
-      if (ok) {
-        tc_fence_after();
-        issue_dp(0);
-        ok = n < 2 || wait_k(1);
-      }
-      if (ok && n > 1) {
-        tc_fence_after();
-        issue_s(1);
-      }
-      for (int j = 0; j < n && ok; ++j) {
-        // V of the next turn is waited for ahead of it.
-        if (j + 1 < n && !(ok = wait_v(j + 1))) break;
-        // dS_j written: dP_j and S_j have been read.
-        if (!(ok = wait(ds_full, j & 1))) break;
-        tc_fence_after();
-        if (j + 1 < n) issue_dp(j + 1);
-        bwd_issue_ts(leader, tmem + 384, tmem + 128 * (j & 1), kn + j % 3 * kTile, idesc_o, j == 0, 0, 4);
-        mma_commit_warp(leader, &k_empty[j % 3]);
-        if (j + 2 < n) {
-          if (!(ok = wait_k(j + 2))) break;
-          tc_fence_after();
-          issue_s(j + 2);
+      int J = 0, busy = 0, nq = 0, nd = 0, jk = 0, jv = 0;
+      bool ok = true;
+      for (int kk = 0, i = bwd_item(s, 0); i < items && ok; i = bwd_item(s, ++kk)) {
+        const Item it = item_at(i);
+        if (it.kr.t_count == 0) continue;
+        if (busy > 0 && !(ok = mbar_wait(q_empty, (busy - 1) & 1, code))) break;
+        load(sq, &tm_q, q_full, it.r0, it.run);
+        ++nq;
+        for (int j = 0; j < it.kr.t_count; ++j, ++J) {
+          const int key0 = (it.kr.t_first + j) * 128;
+          if (J >= 3 && !(ok = mbar_wait(&k_empty[J % 3], (J / 3 - 1) & 1, code))) break;
+          load(sk + (J % 3) * C::kTileBytes, &tm_k, &k_full[J % 3], key0, it.unit);
+          ++jk;
+          if (j == 0) {
+            if (busy > 0 && !(ok = mbar_wait(do_empty, (busy - 1) & 1, code))) break;
+            load(sdo, &tm_do, do_full, it.r0, it.run);
+            ++nd;
+          }
+          if (J >= 2 && !(ok = mbar_wait(&v_empty[J & 1], (J / 2 - 1) & 1, code))) break;
+          load(sv + (J & 1) * C::kTileBytes, &tm_v, &v_full[J & 1], key0, it.unit);
+          ++jv;
         }
+        ++busy;
       }
-      mma_commit_warp(leader, o_done);
-      wait(o_done, 0);
+      // Never leave with copies in flight.
+      if (nq > 0) mbar_wait(q_full, (nq - 1) & 1, code);
+      if (nd > 0) mbar_wait(do_full, (nd - 1) & 1, code);
+      for (int j = max(0, jk - 3); j < jk; ++j) mbar_wait(&k_full[j % 3], (j / 3) & 1, code);
+      for (int j = max(0, jv - 2); j < jv; ++j) mbar_wait(&v_full[j & 1], (j / 2) & 1, code);
     }
+  } else if (warp == 1 || warp == 2) {
+    // Two issuers as above: warp 1 S and dQ, warp 2 dP.
+    const uint32_t leader = lane == 0;
+    const int d_pad = (s.head_dim + 15) / 16 * 16, ksteps = d_pad / 16;
+    const uint32_t idesc_s = idesc_bf16_f32(128, 128, 0);
+    const uint32_t idesc_o = idesc_bf16_f32(128, d_pad, 1);
+    const uint64_t qd = bwd_desc_k(smem_u32(sq)), dd = bwd_desc_k(smem_u32(sdo));
+    const uint64_t kd = bwd_desc_k(smem_u32(sk)), kn = bwd_desc_n<DCH>(smem_u32(sk));
+    const uint64_t vd = bwd_desc_k(smem_u32(sv));
+    constexpr uint32_t kTile = C::kTileBytes >> 4;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, kStatusTimeoutMma)) != 0;
+    };
+    int J = 0, busy = 0;
+    int k_j = 0, k_s = 0, x = 0;  // K slots of dQ's tile J and of S's tile x
+    bool ok = true;
+    for (int kk = 0, i = bwd_item(s, 0); i < items && ok; i = bwd_item(s, ++kk)) {
+      const int n = item_at(i).kr.t_count;
+      if (n == 0) continue;
+      if (warp == 1) {
+        const int x_end = J + n;
+        // S of the next tile into its buffer; the last one frees Q.
+        auto issue_s = [&]() {
+          if (!wait(&k_full[k_s], (x / 3) & 1)) return false;
+          tc_fence_after();
+          bwd_issue_ss<DCH>(leader, tmem + 128 * (x & 1), qd, kd + k_s * kTile, idesc_s, ksteps);
+          mma_commit_warp(leader, &s_full[x & 1]);
+          ++x;
+          if (++k_s == 3) k_s = 0;
+          if (x == x_end) mma_commit_warp(leader, q_empty);
+          return true;
+        };
+        if (!(ok = wait(q_full, busy & 1) && issue_s())) break;
+        if (n > 1 && !(ok = issue_s())) break;
+        for (int j = 0; j < n; ++j, ++J) {
+          // dS_j written: S_j has been read.
+          if (!(ok = wait(&ds_full[J & 1], (J / 2) & 1))) break;
+          tc_fence_after();
+          bwd_issue_ts<0, 4>(leader, tmem + 384, tmem + 128 * (J & 1), kn + k_j * kTile, idesc_o, j == 0);
+          mma_commit_warp(leader, &k_empty[k_j]);
+          if (++k_j == 3) k_j = 0;
+          if (x < x_end && !(ok = issue_s())) break;
+        }
+        if (!ok) break;
+        mma_commit_warp(leader, o_done);
+      } else {
+        if (!(ok = wait(do_full, busy & 1))) break;
+        for (int j = 0; j < n; ++j, ++J) {
+          if (!(ok = wait(&v_full[J & 1], (J / 2) & 1))) break;
+          // The previous tile's dP has been read.
+          if (J > 0 && !(ok = wait(&ds_full[(J - 1) & 1], ((J - 1) / 2) & 1))) break;
+          tc_fence_after();
+          bwd_issue_ss<DCH>(leader, tmem + 256, dd, vd + (J & 1) * kTile, idesc_s, ksteps);
+          mma_commit_warp(leader, dp_full);
+          mma_commit_warp(leader, &v_empty[J & 1]);
+        }
+        if (!ok) break;
+        mma_commit_warp(leader, do_empty);
+      }
+      ++busy;
+    }
+    // Every product finished before TMEM is freed.
+    mma_commit_warp(leader, drain);
+    wait(drain, 0);
   } else if (warp >= 4) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kBwRegsHigh));
     const int h = (warp - 4) >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-    const float* st = p.stats + ((long long)run * s.tiles + t) * 256;
+    const int d_pad = (s.head_dim + 15) / 16 * 16;
+    int J = 0, busy = 0;
+    bool ok = true;
+    for (int kk = 0, i = bwd_item(s, 0); i < items && ok; i = bwd_item(s, ++kk)) {
+    const Item it = item_at(i);
+    const float* st = p.stats + ((long long)it.run * s.tiles + it.tile) * 256;
     const float nlse = st[r], delta = st[128 + r];
     int lo = 0, hi = -1;
-    if (r < nr) {
-      const int qpos = s.kv_len - s.q_len + (r0 + r) % s.q_len;
+    if (r < it.nr) {
+      const int qpos = s.kv_len - s.q_len + (it.r0 + r) % s.q_len;
       lo = first_key(ms, qpos);
       hi = last_key(ms, qpos);
     }
-    bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      const int key0 = (kr.t_first + j) * 128;
-      const bool need_mask = !(key0 >= kr.all_lo && key0 + 127 <= kr.all_hi);
+    for (int j = 0; j < it.kr.t_count; ++j, ++J) {
+      const int key0 = (it.kr.t_first + j) * 128;
+      const bool need_mask = !(key0 >= it.kr.all_lo && key0 + 127 <= it.kr.all_hi);
       const int clo = max(lo - key0, 0), chi = min(hi - key0, 127);
       const int vlo = chi >= clo ? clo : 128;
       const unsigned vspan = chi >= clo ? (unsigned)(chi - clo) : 0u;
-      const uint32_t s_tm = tmem + lane_base + 128 * (j & 1) + 64 * h;
+      const uint32_t s_tm = tmem + lane_base + 128 * (J & 1) + 64 * h;
       f2 keep[32];
-      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[j & 1], (j / 2) & 1, kStatusTimeoutSoftmax));
+      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[J & 1], (J / 2) & 1, kStatusTimeoutSoftmax));
       if (!ok) break;
       tc_fence_after();
       uint32_t b0[32], b1[32];
@@ -720,7 +814,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
       probs(b0, 0);
       tmem_ld_wait();
       probs(b1, 1);
-      ok = __all_sync(0xffffffffu, mbar_wait(dp_full, j & 1, kStatusTimeoutSoftmax));
+      ok = __all_sync(0xffffffffu, mbar_wait(dp_full, J & 1, kStatusTimeoutSoftmax));
       if (!ok) break;
       tc_fence_after();
       uint32_t pk[16];
@@ -736,18 +830,19 @@ __global__ void __launch_bounds__(kBwThreads, 1)
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ds_full);
+      if (lane == 0) mbar_arrive(&ds_full[J & 1]);
     }
-    if (n > 0 && ok)
-      ok = __all_sync(0xffffffffu, mbar_wait(o_done, 0, kStatusTimeoutEpilogue));
-    if (ok) {
+    if (!ok) break;
+    if (it.kr.t_count > 0) {
+      ok = __all_sync(0xffffffffu, mbar_wait(o_done, busy & 1, kStatusTimeoutEpilogue));
+      if (!ok) break;
+      ++busy;
       tc_fence_after();
-      uint8_t* stage = sk + (warp - 4) * 4096;
-      const int d_pad = (s.head_dim + 15) / 16 * 16, c0 = 64 * h;
-      if (c0 < d_pad && quarter * 32 < nr)
-        bwd_store_box(&tm_dq, stage, tmem + lane_base + 384, c0, min(64, d_pad - c0),
-                      r0 + quarter * 32, run, p.scale, n == 0, lane);
-      if (lane == 0) bulk_wait_all();
+    }
+    // Each warpgroup stores its half of the columns.
+    if (quarter * 32 < it.nr)
+      bwd_store_row(p.dq + ((long long)it.run * s.run + it.r0 + r) * s.head_dim, tmem + lane_base + 384,
+                    64 * h, min(64 * h + 64, d_pad), s.head_dim, p.scale, it.kr.t_count == 0, r < it.nr);
     }
   }
   tc_fence_before();

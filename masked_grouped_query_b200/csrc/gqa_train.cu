@@ -56,7 +56,7 @@ int bwd_shape(int batch, int q_len, int kv_len, int hq, int hkv, int d, int caus
   if (d < 8 || d > 256 || d % 8 != 0) return GQA_ATTN_ERR_HEAD_DIM;
   const int group = hq / hkv;
   // Row and key indexes are 32-bit, with room for the last tile's padding.
-  constexpr long long kMost = 0x7fffff00LL;
+  constexpr long long kMost = 0x7fff0000LL;
   if ((long long)group * q_len > kMost || kv_len > kMost || (long long)batch * hq > kMost)
     return GQA_ATTN_ERR_TOO_LARGE;
   s->q_len = q_len;
@@ -115,32 +115,29 @@ int bwd_sm100_setup(K kernel, int bytes, int device, bool* done) {
 }
 
 template <int DCH, bool kCap>
-int launch_bwd_sm100(const BwdParams& p, int device, cudaStream_t st) {
+int launch_bwd_sm100(const BwdParams& p, int device, int sms, cudaStream_t st) {
   using C = BwdCfg<DCH>;
   static bool done_kv[kMaxDevices], done_q[kMaxDevices];
   int rc = bwd_sm100_setup(bwd_dkdv_kernel<DCH, kCap>, C::kSmemBytes, device, done_kv);
   if (rc == GQA_ATTN_OK) rc = bwd_sm100_setup(bwd_dq_kernel<DCH, kCap>, C::kSmemBytes, device, done_q);
   if (rc != GQA_ATTN_OK) return rc;
   const BwdShape& s = p.sh;
-  CUtensorMap q, dout, k, v, dq, dk, dv;
+  CUtensorMap q, dout, k, v;
   const struct {
     CUtensorMap* map;
     const void* base;
     bool rows;
-    int box;
-  } maps[7] = {{&q, p.q, true, 128},     {&dout, p.dout, true, 128}, {&k, p.k, false, 128},
-               {&v, p.v, false, 128},    {&dq, p.dq, true, 32},      {&dk, p.dk, false, 32},
-               {&dv, p.dv, false, 32}};
+  } maps[4] = {{&q, p.q, true}, {&dout, p.dout, true}, {&k, p.k, false}, {&v, p.v, false}};
   for (const auto& m : maps)
     if ((rc = gqa_host::tensor_map(m.map, m.base, s.head_dim, m.rows ? s.run : s.kv_len,
-                                   m.rows ? s.runs : s.units, m.box)) != GQA_ATTN_OK)
+                                   m.rows ? s.runs : s.units, 128)) != GQA_ATTN_OK)
       return rc;
-  const long long key_tiles = s.units * ceil_div(s.kv_len, 128);
-  bwd_dkdv_kernel<DCH, kCap><<<(unsigned)key_tiles, kBwThreads, C::kSmemBytes, st>>>(q, dout, k, v, dk,
-                                                                                  dv, p);
+  const long long key_tiles = s.units * ceil_div(s.kv_len, 128), row_tiles = s.runs * s.tiles;
+  const unsigned kv_grid = (unsigned)(key_tiles < sms ? key_tiles : sms);
+  bwd_dkdv_kernel<DCH, kCap><<<kv_grid, kBwThreads, C::kSmemBytes, st>>>(q, dout, k, v, p);
   if ((rc = launched("launch(backward dK dV)")) != GQA_ATTN_OK) return rc;
-  bwd_dq_kernel<DCH, kCap><<<(unsigned)(s.runs * s.tiles), kBwThreads, C::kSmemBytes, st>>>(q, dout, k,
-                                                                                         v, dq, p);
+  const unsigned q_grid = (unsigned)(row_tiles < sms ? row_tiles : sms);
+  bwd_dq_kernel<DCH, kCap><<<q_grid, kBwThreads, C::kSmemBytes, st>>>(q, dout, k, v, p);
   return launched("launch(backward dQ)");
 }
 
@@ -260,10 +257,10 @@ int gqa_attn_bwd(const void* dout, const void* q, const void* k, const void* v, 
   if (head_dim > 128) return launch_bwd_mma<16>(p, device, st);
   if (gqa_host::forced_path() == 1) return launch_bwd_mma<8>(p, device, st);
   if (head_dim <= 64)
-    return p.softcap ? launch_bwd_sm100<1, true>(p, device, st)
-                     : launch_bwd_sm100<1, false>(p, device, st);
-  return p.softcap ? launch_bwd_sm100<2, true>(p, device, st)
-                   : launch_bwd_sm100<2, false>(p, device, st);
+    return p.softcap ? launch_bwd_sm100<1, true>(p, device, sms, st)
+                     : launch_bwd_sm100<1, false>(p, device, sms, st);
+  return p.softcap ? launch_bwd_sm100<2, true>(p, device, sms, st)
+                   : launch_bwd_sm100<2, false>(p, device, sms, st);
 }
 
 int gqa_attn_rotary(const void* q, const void* k, void* q_out, void* k_out, const void* positions,
