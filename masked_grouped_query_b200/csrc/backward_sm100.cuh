@@ -5,9 +5,8 @@
 // items (a key tile, or a row tile, of 128) in rounds of the grid; barriers,
 // TMEM and the rings live across items, so the next item's loads and first
 // products run under the current one's last steps and its stores:
-//   warp 0      TMA loader (and the statistics' bulk copies);
+//   warps 0, 3  TMA loaders (warp 0 the statistics' bulk copies too);
 //   warp 1      TMEM allocator; warps 1 and 2 issue the tcgen05.mma (a lane each);
-//   warp 3      idle (it completes warpgroup 0 for the register split);
 //   warps 4-11  elementwise work: warpgroup h takes columns [64 h, 64 h + 64)
 //               of the 128 x 128 tiles, a thread one lane (row) of them.
 //
@@ -57,7 +56,11 @@ struct BwdCfg {
   static constexpr int kStats = kRing2 + 2 * kTileBytes;  // two slots of 256 floats
   static constexpr int kBars = kStats + 2 * 1024;
   static constexpr int kNumBars = 26;
-  static constexpr int kSmemBytes = kBars + kNumBars * 8 + 16;
+  // Output boxes, 4 KB for each of the eight elementwise warps: with 64
+  // columns there is room for them, with 128 they take the place of the
+  // resident operand of dP (V or dO), whose next load then waits for them.
+  static constexpr int kStage = DCH == 1 ? (kBars + kNumBars * 8 + 16 + 1023) / 1024 * 1024 : kTileBytes;
+  static constexpr int kSmemBytes = DCH == 1 ? kStage + 8 * 4096 : kBars + kNumBars * 8 + 16;
 };
 
 // Whether any row of a row tile fails to see any key of a key tile: only then
@@ -84,10 +87,9 @@ __device__ __forceinline__ bool bwd_need_mask(const BwdShape& s, const MaskSpec&
 }
 
 // P of 32 columns from 32 raw scores (nl: -lse of their rows, in pairs), and
-// with a softcap the factors 1 - tanh^2 that dS takes.  The last pairs of
-// every 16 take 2^x from the FMA pipe: MUFU alone would need 1024 cycles for
-// a 128 x 128 tile, half of the tensor core's time for the tile's products.
-constexpr int kBwEmuFrom = 13;
+// with a softcap the factors 1 - tanh^2 that dS takes.  Every 2^x is MUFU's:
+// moving 2 to 6 of 16 pairs to the FMA pipe, as the forward kernel does with
+// 2, measured from 1% faster to 2% slower.
 template <bool kCap>
 __device__ __forceinline__ void bwd_probs(const BwdParams& p, const uint32_t (&s)[32],
                                           const f2 (&nl)[16], f2 (&pr)[16], f2 (&fac)[16]) {
@@ -96,7 +98,7 @@ __device__ __forceinline__ void bwd_probs(const BwdParams& p, const uint32_t (&s
 #pragma unroll
     for (int c = 0; c < 16; ++c) {
       const f2 y = f2_fma(f2_pack(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), sc, nl[c]);
-      pr[c] = c >= kBwEmuFrom ? exp2_poly_x2(y) : exp2_mufu_x2(y);
+      pr[c] = exp2_mufu_x2(y);
     }
   } else {
     float am = 0.f;
@@ -106,23 +108,24 @@ __device__ __forceinline__ void bwd_probs(const BwdParams& p, const uint32_t (&s
     const bool small = __all_sync(0xffffffffu, am * p.cap_in <= 0.5f);
     const f2 co = f2_pack(p.cap_out, p.cap_out), one = f2_pack(1.f, 1.f);
     if (small) {
-      const f2 ci = f2_pack(p.cap_in, p.cap_in), nci = f2_pack(-p.cap_in, -p.cap_in);
-      const f2 c3 = f2_pack(kTanh9C3, kTanh9C3), c5 = f2_pack(kTanh9C5, kTanh9C5);
-      const f2 c7 = f2_pack(kTanh9C7, kTanh9C7), c9 = f2_pack(kTanh9C9, kTanh9C9);
+      // tanh(x cap_in) as x Q(x^2), cap_in folded into the coefficients.
+      const float i2 = p.cap_in * p.cap_in;
+      const float q1 = kTanhC1 * p.cap_in, q3 = kTanhC3 * p.cap_in * i2;
+      const float q5 = kTanhC5 * p.cap_in * i2 * i2, q7 = kTanhC7 * p.cap_in * i2 * i2 * i2;
+      const f2 c1 = f2_pack(q1, q1), c3 = f2_pack(q3, q3), c5 = f2_pack(q5, q5), c7 = f2_pack(q7, q7);
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
         const f2 x = f2_pack(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
-        const f2 y = f2_mul(x, ci), y2 = f2_mul(y, y);
-        const f2 q = f2_fma(f2_fma(f2_fma(f2_fma(c9, y2, c7), y2, c5), y2, c3), y2, one);
-        const f2 t = f2_mul(y, q);
+        const f2 x2 = f2_mul(x, x);
+        const f2 t = f2_mul(x, f2_fma(f2_fma(f2_fma(c7, x2, c5), x2, c3), x2, c1));
         pr[c] = exp2_mufu_x2(f2_fma(co, t, nl[c]));
-        fac[c] = f2_fma(t, f2_mul(f2_mul(x, nci), q), one);
+        fac[c] = f2_fma(t, t ^ 0x8000000080000000ull, one);
       }
     } else {
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
-        const float a = tanh_accurate(__uint_as_float(s[2 * c]) * p.cap_in);
-        const float b = tanh_accurate(__uint_as_float(s[2 * c + 1]) * p.cap_in);
+        const float a = tanh_large(__uint_as_float(s[2 * c]) * p.cap_in);
+        const float b = tanh_large(__uint_as_float(s[2 * c + 1]) * p.cap_in);
         pr[c] = exp2_mufu_x2(f2_fma(co, f2_pack(a, b), nl[c]));
         fac[c] = f2_pack(fmaf(-a, a, 1.f), fmaf(-b, b, 1.f));
       }
@@ -162,31 +165,55 @@ __device__ __forceinline__ void bwd_load32(const float* src, f2 (&v)[16]) {
   }
 }
 
-// This thread's row of an fp32 accumulator in TMEM, columns [c0, c1) (whole
-// 16s; `cols` of them exist), scaled and rounded to bf16.  Stored from
-// registers, 32 bytes at a time: shared memory has no room to stage a tile
-// next to the rings, and the next item's loads are already under way.
-__device__ __forceinline__ void bwd_store_row(__nv_bfloat16* dst, uint32_t tm, int c0, int c1,
-                                              int cols, float scale, bool zero, bool live) {
-  for (int c = c0; c < c1; c += 16) {
-    uint32_t v[16];
-    if (zero) {
+// 64 columns of a warp's 32 rows of an fp32 accumulator at tm, scaled and
+// rounded to bf16, through a swizzled 32-row box in shared memory and one TMA
+// store (rows and columns outside the tensor are not written; columns of the
+// accumulator past head_dim hold whatever TMEM held).  `again`: the box's
+// previous store, of this item, may still be reading it.  Items of one length
+// finish together on all SMs, and their stores then wait for L2: TMA stores
+// leave these warps free meanwhile (from registers, in whole lines or not,
+// they took 1.5 to 2 times as long on the encoder shape).
+__device__ __forceinline__ void bwd_store_box(const CUtensorMap* map, uint8_t* stage, uint32_t tm,
+                                              int x, int row, int outer, float scale, bool zero,
+                                              bool again, int lane) {
+  uint32_t a[32], b[32], w[32];
+  tmem_ld32(tm, a);
+  tmem_ld32(tm + 32, b);
+  tmem_ld_wait();
 #pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = 0u;
-    } else {
-      tmem_ld16(tm + c, v);
-      tmem_ld_wait();
-    }
+  for (int e = 0; e < 16; ++e) {
+    w[e] = zero ? 0u : pack_bf16(__uint_as_float(a[2 * e]) * scale, __uint_as_float(a[2 * e + 1]) * scale);
+    w[16 + e] = zero ? 0u : pack_bf16(__uint_as_float(b[2 * e]) * scale, __uint_as_float(b[2 * e + 1]) * scale);
+  }
+  if (again) {
+    if (lane == 0) bulk_wait_read();
+    __syncwarp();
+  }
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      uint32_t w[4];
+  for (int g = 0; g < 8; ++g)
+    *reinterpret_cast<uint4*>(stage + sw128(lane, g)) =
+        make_uint4(w[4 * g], w[4 * g + 1], w[4 * g + 2], w[4 * g + 3]);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_3d(map, stage, x, row, outer);
+    bulk_commit();
+  }
+}
+
+// Bits lo..hi of a word (none when hi < lo, or outside 0..31).
+__device__ __forceinline__ uint32_t bwd_bits(int lo, int hi) {
+  lo = max(lo, 0);
+  hi = min(hi, 31);
+  return hi < lo ? 0u : (0xffffffffu >> (31 - hi)) & (0xffffffffu << lo);
+}
+// p with the columns whose bit is not set as zeros.
+__device__ __forceinline__ void bwd_hide(f2 (&pr)[16], uint32_t seen) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        w[e] = pack_bf16(__uint_as_float(v[8 * g + 2 * e]) * scale,
-                         __uint_as_float(v[8 * g + 2 * e + 1]) * scale);
-      if (live && c + 8 * g < cols)
-        *reinterpret_cast<uint4*>(dst + c + 8 * g) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
+  for (int c = 0; c < 16; ++c) {
+    float a, b;
+    f2_unpack(pr[c], a, b);
+    pr[c] = f2_pack(seen & (1u << (2 * c)) ? a : 0.f, seen & (2u << (2 * c)) ? b : 0.f);
   }
 }
 
@@ -239,6 +266,7 @@ template <int DCH, bool kCap>
 __global__ void __launch_bounds__(kBwThreads, 1)
     bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                    const __grid_constant__ CUtensorMap tm_dk, const __grid_constant__ CUtensorMap tm_dv,
                     const BwdParams p) {
   using C = BwdCfg<DCH>;
   const BwdShape& s = p.sh;
@@ -274,7 +302,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
     mbar_init(k_empty, 1);
     mbar_init(drain, 2);
     mbar_init(v_full, 1);
-    mbar_init(v_empty, 1);
+    mbar_init(v_empty, 1 + 8);  // the last dP^T, and the output boxes
     for (int i = 0; i < 3; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
@@ -320,46 +348,47 @@ __global__ void __launch_bounds__(kBwThreads, 1)
   };
 
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBwRegsLow));
-  if (warp == 0) {
+  if (warp == 0 || warp == 3) {
+    // Two loaders: warp 0 K, Q and the statistics, warp 3 V and dO (V waits
+    // for the output boxes).
     if (lane == 0) {
-      tma_prefetch_map(&tm_q);
-      tma_prefetch_map(&tm_do);
-      tma_prefetch_map(&tm_k);
-      tma_prefetch_map(&tm_v);
       constexpr uint32_t code = kStatusTimeoutProducer;
       auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int row, int outer) {
         mbar_arrive_expect_tx(bar, C::kTileBytes);
         for (int c = 0; c < DCH; ++c)
           tma_load_3d(dst + c * C::kBoxBytes, map, bar, c * 64, row, outer);
       };
-      int J = 0, busy = 0;         // row tiles and items so far
-      int jq = 0, jd = 0, js = 0;  // loads issued
-      int nk = 0, nv = 0;
+      const bool first = warp == 0;
+      tma_prefetch_map(first ? &tm_q : &tm_do);
+      tma_prefetch_map(first ? &tm_k : &tm_v);
+      int J = 0, busy = 0;        // row tiles and items so far
+      int n1 = 0, n2 = 0, n3 = 0;  // loads issued: K or V, Q or dO, statistics
       bool ok = true;
       for (int kk = 0, i = bwd_item(s, 0); i < items && ok; i = bwd_item(s, ++kk)) {
         const Item it = item_at(i);
         if (it.n == 0) continue;
-        if (busy > 0 && !(ok = mbar_wait(k_empty, (busy - 1) & 1, code))) break;
-        load(sk, &tm_k, k_full, it.k0, it.unit);
-        ++nk;
+        uint64_t* const free1 = first ? k_empty : v_empty;
+        if (busy > 0 && !(ok = mbar_wait(free1, (busy - 1) & 1, code))) break;
+        if (first) load(sk, &tm_k, k_full, it.k0, it.unit);
+        else load(sv, &tm_v, v_full, it.k0, it.unit);
+        ++n1;
         int run = it.unit * s.runs_per_unit, t = it.first;
         for (int j = 0; j < it.n; ++j, ++J) {
           const int q3 = J % 3, d2 = J & 1;
-          if (J >= 3 && !(ok = mbar_wait(&q_empty[q3], (J / 3 - 1) & 1, code))) break;
-          load(sq + q3 * C::kTileBytes, &tm_q, &q_full[q3], t * 128, run);
-          ++jq;
-          if (j == 0) {
-            if (busy > 0 && !(ok = mbar_wait(v_empty, (busy - 1) & 1, code))) break;
-            load(sv, &tm_v, v_full, it.k0, it.unit);
-            ++nv;
+          if (first) {
+            if (J >= 3 && !(ok = mbar_wait(&q_empty[q3], (J / 3 - 1) & 1, code))) break;
+            load(sq + q3 * C::kTileBytes, &tm_q, &q_full[q3], t * 128, run);
+            ++n2;
+            if (J >= 2 && !(ok = mbar_wait(&st_empty[d2], (J / 2 - 1) & 1, code))) break;
+            mbar_arrive_expect_tx(&st_full[d2], 1024);
+            bulk_load(stats + d2 * 256, p.stats + ((long long)run * s.tiles + t) * 256, 1024,
+                      &st_full[d2]);
+            ++n3;
+          } else {
+            if (J >= 2 && !(ok = mbar_wait(&do_empty[d2], (J / 2 - 1) & 1, code))) break;
+            load(sdo + d2 * C::kTileBytes, &tm_do, &do_full[d2], t * 128, run);
+            ++n2;
           }
-          if (J >= 2 && !(ok = mbar_wait(&do_empty[d2], (J / 2 - 1) & 1, code))) break;
-          load(sdo + d2 * C::kTileBytes, &tm_do, &do_full[d2], t * 128, run);
-          ++jd;
-          if (J >= 2 && !(ok = mbar_wait(&st_empty[d2], (J / 2 - 1) & 1, code))) break;
-          mbar_arrive_expect_tx(&st_full[d2], 1024);
-          bulk_load(stats + d2 * 256, p.stats + ((long long)run * s.tiles + t) * 256, 1024, &st_full[d2]);
-          ++js;
           if (++t == it.first + it.count) {
             t = it.first;
             ++run;
@@ -368,11 +397,12 @@ __global__ void __launch_bounds__(kBwThreads, 1)
         ++busy;
       }
       // Never leave with copies in flight.
-      if (nk > 0) mbar_wait(k_full, (nk - 1) & 1, code);
-      if (nv > 0) mbar_wait(v_full, (nv - 1) & 1, code);
-      for (int j = max(0, jq - 3); j < jq; ++j) mbar_wait(&q_full[j % 3], (j / 3) & 1, code);
-      for (int j = max(0, jd - 2); j < jd; ++j) mbar_wait(&do_full[j & 1], (j / 2) & 1, code);
-      for (int j = max(0, js - 2); j < js; ++j) mbar_wait(&st_full[j & 1], (j / 2) & 1, code);
+      if (n1 > 0) mbar_wait(first ? k_full : v_full, (n1 - 1) & 1, code);
+      if (first)
+        for (int j = max(0, n2 - 3); j < n2; ++j) mbar_wait(&q_full[j % 3], (j / 3) & 1, code);
+      else
+        for (int j = max(0, n2 - 2); j < n2; ++j) mbar_wait(&do_full[j & 1], (j / 2) & 1, code);
+      for (int j = max(0, n3 - 2); j < n3; ++j) mbar_wait(&st_full[j & 1], (j / 2) & 1, code);
     }
   } else if (warp == 1 || warp == 2) {
     // Two issuers: warp 1 the products S^T and dV, warp 2 dP^T and dK.  While
@@ -456,20 +486,16 @@ __global__ void __launch_bounds__(kBwThreads, 1)
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     const uint32_t s_tm = tmem + lane_base + 64 * h, dp_tm = s_tm + 128;
     const MaskSpec ms = bwd_mask(s);
-    const int d_pad = (s.head_dim + 15) / 16 * 16;
     int J = 0, busy = 0;
     bool ok = true;
-    for (int kk = 0, i = bwd_item(s, 0); i < items && ok; i = bwd_item(s, ++kk)) {
-    const Item it = item_at(i);
+    int i = bwd_item(s, 0);
+    Item it = item_at(i);
+    for (int kk = 1; i < items && ok; ++kk) {
     const int key = it.k0 + quarter * 32 + lane;
-    // Queries that see this lane's key: [qlo, qlo + qspan] (none past kv_len).
+    // Queries that see this lane's key: [qlo, qhi] (none past kv_len).
     int qlo, qhi;
     bwd_query_range(s, key, key, qlo, qhi);
-    if (key >= s.kv_len || qhi < qlo) {
-      qlo = 0x7fffffff;
-      qhi = 0x7fffffff;
-    }
-    const unsigned qspan = (unsigned)(qhi - qlo);
+    if (key >= s.kv_len) qhi = -1;
     int t = it.first;
     for (int j = 0; j < it.n; ++j, ++J) {
       const int r0 = t * 128, nr = min(128, s.run - r0);
@@ -477,32 +503,41 @@ __global__ void __launch_bounds__(kBwThreads, 1)
       const uint32_t par = J & 1, dpar = (J / 2) & 1;
       f2 keep[32];
       const float* st = stats + par * 256 + 64 * h;
-      ok = mbar_wait(&st_full[par], dpar, kStatusTimeoutSoftmax) &&
-           mbar_wait(&s_full[par], dpar, kStatusTimeoutSoftmax);
-      ok = __all_sync(0xffffffffu, ok);
+      f2 nl[16];
+      ok = __all_sync(0xffffffffu, mbar_wait(&st_full[par], dpar, kStatusTimeoutSoftmax));
+      if (!ok) break;
+      bwd_load32(st, nl);
+      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[par], dpar, kStatusTimeoutSoftmax));
       if (!ok) break;
       tc_fence_after();
       uint32_t b0[32], b1[32];
       tmem_ld32(s_tm, b0);
-      int qi = need_mask ? (r0 + 64 * h) % s.q_len : 0;  // query of the next column
+      uint32_t seen[2] = {0u, 0u};  // this lane's key by the columns of its half
+      if (need_mask) {
+        const int c0 = r0 + 64 * h;
+        if (s.run == s.q_len) {
+          seen[0] = bwd_bits(qlo - c0, qhi - c0);
+          seen[1] = bwd_bits(qlo - c0 - 32, qhi - c0 - 32);
+        } else {  // several heads in the tile: query by query
+          int qi = c0 % s.q_len;
+#pragma unroll 1
+          for (int c = 0; c < 32; ++c) {
+            if (qi >= qlo && qi <= qhi) seen[0] |= 1u << c;
+            if (++qi == s.q_len) qi = 0;
+          }
+#pragma unroll 1
+          for (int c = 0; c < 32; ++c) {
+            if (qi >= qlo && qi <= qhi) seen[1] |= 1u << c;
+            if (++qi == s.q_len) qi = 0;
+          }
+        }
+      }
       // P of columns 32 g .. 32 g + 31 of this half, into TMEM columns
       // [16 g, 16 g + 16) of it, whose scores have been read.
       auto probs = [&](const uint32_t(&sv32)[32], int g) {
-        f2 nl[16], pr[16], fac[16];
-        bwd_load32(st + 32 * g, nl);
+        f2 pr[16], fac[16];
         bwd_probs<kCap>(p, sv32, nl, pr, fac);
-        if (need_mask) {
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            float a, b;
-            f2_unpack(pr[c], a, b);
-            if ((unsigned)(qi - qlo) > qspan) a = 0.f;
-            if (++qi == s.q_len) qi = 0;
-            if ((unsigned)(qi - qlo) > qspan) b = 0.f;
-            if (++qi == s.q_len) qi = 0;
-            pr[c] = f2_pack(a, b);
-          }
-        }
+        if (need_mask) bwd_hide(pr, seen[g]);
         uint32_t pk[16];
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
@@ -519,6 +554,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(p_half);
+      bwd_load32(st + 32, nl);
       probs(b1, 1);
       tmem_st_wait();
       tc_fence_before();
@@ -549,6 +585,8 @@ __global__ void __launch_bounds__(kBwThreads, 1)
       if (++t == it.first + it.count) t = it.first;
     }
     if (!ok) break;
+    const int next = bwd_item(s, kk);
+    const Item next_it = item_at(next);  // ahead of the wait: divisions
     if (it.n > 0) {
       ok = __all_sync(0xffffffffu, mbar_wait(o_done, busy & 1, kStatusTimeoutEpilogue));
       if (!ok) break;
@@ -557,11 +595,20 @@ __global__ void __launch_bounds__(kBwThreads, 1)
     }
     // Warpgroup 0 stores dV, warpgroup 1 dK.  The next item's first products
     // into them follow this thread's next P and dS arrivals.
-    if (it.k0 + quarter * 32 < s.kv_len)
-      bwd_store_row((h ? p.dk : p.dv) + ((long long)it.unit * s.kv_len + key) * s.head_dim,
-                    tmem + lane_base + 256 + 128 * h, 0, d_pad, s.head_dim, h ? p.scale : 1.f,
-                    it.n == 0, key < s.kv_len);
+    uint8_t* stage = smem + C::kStage + (warp - 4) * 4096;
+    const int row0 = it.k0 + quarter * 32;
+#pragma unroll 1
+    for (int c0 = 0; c0 < s.head_dim && row0 < s.kv_len; c0 += 64)
+      bwd_store_box(h ? &tm_dk : &tm_dv, stage, tmem + lane_base + 256 + 128 * h + c0, c0, row0,
+                    it.unit, h ? p.scale : 1.f, it.n == 0, c0 > 0, lane);
+    if (lane == 0) {
+      bulk_wait_read();  // the box goes back to the loader, or to the next item
+      if (it.n > 0) mbar_arrive(v_empty);
     }
+    i = next;
+    it = next_it;
+    }
+    if (lane == 0) bulk_wait_all();  // stores done before the CTA exits
   }
   tc_fence_before();
   __syncthreads();
@@ -576,7 +623,7 @@ template <int DCH, bool kCap>
 __global__ void __launch_bounds__(kBwThreads, 1)
     bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                   const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                  const BwdParams p) {
+                  const __grid_constant__ CUtensorMap tm_dq, const BwdParams p) {
   using C = BwdCfg<DCH>;
   const BwdShape& s = p.sh;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -619,7 +666,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
     mbar_init(o_done, 1);
     mbar_init(q_empty, 1);
     mbar_init(do_full, 1);
-    mbar_init(do_empty, 1);
+    mbar_init(do_empty, 1 + 8);  // the last dP, and the output boxes
     mbar_init(drain, 2);
     fence_barrier_init();
   }
@@ -653,47 +700,48 @@ __global__ void __launch_bounds__(kBwThreads, 1)
   };
 
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBwRegsLow));
-  if (warp == 0) {
+  if (warp == 0 || warp == 3) {
+    // Two loaders: warp 0 Q and K, warp 3 dO and V (dO waits for the output
+    // boxes).
     if (lane == 0) {
-      tma_prefetch_map(&tm_q);
-      tma_prefetch_map(&tm_do);
-      tma_prefetch_map(&tm_k);
-      tma_prefetch_map(&tm_v);
       constexpr uint32_t code = kStatusTimeoutProducer;
       auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int row, int outer) {
         mbar_arrive_expect_tx(bar, C::kTileBytes);
         for (int c = 0; c < DCH; ++c)
           tma_load_3d(dst + c * C::kBoxBytes, map, bar, c * 64, row, outer);
       };
-      int J = 0, busy = 0, nq = 0, nd = 0, jk = 0, jv = 0;
+      const bool first = warp == 0;
+      tma_prefetch_map(first ? &tm_q : &tm_do);
+      tma_prefetch_map(first ? &tm_k : &tm_v);
+      int J = 0, busy = 0, n1 = 0, n2 = 0;
       bool ok = true;
       for (int kk = 0, i = bwd_item(s, 0); i < items && ok; i = bwd_item(s, ++kk)) {
         const Item it = item_at(i);
         if (it.kr.t_count == 0) continue;
-        if (busy > 0 && !(ok = mbar_wait(q_empty, (busy - 1) & 1, code))) break;
-        load(sq, &tm_q, q_full, it.r0, it.run);
-        ++nq;
+        uint64_t* const free1 = first ? q_empty : do_empty;
+        if (busy > 0 && !(ok = mbar_wait(free1, (busy - 1) & 1, code))) break;
+        if (first) load(sq, &tm_q, q_full, it.r0, it.run);
+        else load(sdo, &tm_do, do_full, it.r0, it.run);
+        ++n1;
         for (int j = 0; j < it.kr.t_count; ++j, ++J) {
-          const int key0 = (it.kr.t_first + j) * 128;
-          if (J >= 3 && !(ok = mbar_wait(&k_empty[J % 3], (J / 3 - 1) & 1, code))) break;
-          load(sk + (J % 3) * C::kTileBytes, &tm_k, &k_full[J % 3], key0, it.unit);
-          ++jk;
-          if (j == 0) {
-            if (busy > 0 && !(ok = mbar_wait(do_empty, (busy - 1) & 1, code))) break;
-            load(sdo, &tm_do, do_full, it.r0, it.run);
-            ++nd;
+          const int key0 = (it.kr.t_first + j) * 128, k3 = J % 3, v2 = J & 1;
+          if (first) {
+            if (J >= 3 && !(ok = mbar_wait(&k_empty[k3], (J / 3 - 1) & 1, code))) break;
+            load(sk + k3 * C::kTileBytes, &tm_k, &k_full[k3], key0, it.unit);
+          } else {
+            if (J >= 2 && !(ok = mbar_wait(&v_empty[v2], (J / 2 - 1) & 1, code))) break;
+            load(sv + v2 * C::kTileBytes, &tm_v, &v_full[v2], key0, it.unit);
           }
-          if (J >= 2 && !(ok = mbar_wait(&v_empty[J & 1], (J / 2 - 1) & 1, code))) break;
-          load(sv + (J & 1) * C::kTileBytes, &tm_v, &v_full[J & 1], key0, it.unit);
-          ++jv;
+          ++n2;
         }
         ++busy;
       }
       // Never leave with copies in flight.
-      if (nq > 0) mbar_wait(q_full, (nq - 1) & 1, code);
-      if (nd > 0) mbar_wait(do_full, (nd - 1) & 1, code);
-      for (int j = max(0, jk - 3); j < jk; ++j) mbar_wait(&k_full[j % 3], (j / 3) & 1, code);
-      for (int j = max(0, jv - 2); j < jv; ++j) mbar_wait(&v_full[j & 1], (j / 2) & 1, code);
+      if (n1 > 0) mbar_wait(first ? q_full : do_full, (n1 - 1) & 1, code);
+      if (first)
+        for (int j = max(0, n2 - 3); j < n2; ++j) mbar_wait(&k_full[j % 3], (j / 3) & 1, code);
+      else
+        for (int j = max(0, n2 - 2); j < n2; ++j) mbar_wait(&v_full[j & 1], (j / 2) & 1, code);
     }
   } else if (warp == 1 || warp == 2) {
     // Two issuers as above: warp 1 S and dQ, warp 2 dP.
@@ -764,11 +812,11 @@ __global__ void __launch_bounds__(kBwThreads, 1)
     const int h = (warp - 4) >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-    const int d_pad = (s.head_dim + 15) / 16 * 16;
     int J = 0, busy = 0;
     bool ok = true;
-    for (int kk = 0, i = bwd_item(s, 0); i < items && ok; i = bwd_item(s, ++kk)) {
-    const Item it = item_at(i);
+    int i = bwd_item(s, 0);
+    Item it = item_at(i);
+    for (int kk = 1; i < items && ok; ++kk) {
     const float* st = p.stats + ((long long)it.run * s.tiles + it.tile) * 256;
     const float nlse = st[r], delta = st[128 + r];
     int lo = 0, hi = -1;
@@ -780,9 +828,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
     for (int j = 0; j < it.kr.t_count; ++j, ++J) {
       const int key0 = (it.kr.t_first + j) * 128;
       const bool need_mask = !(key0 >= it.kr.all_lo && key0 + 127 <= it.kr.all_hi);
-      const int clo = max(lo - key0, 0), chi = min(hi - key0, 127);
-      const int vlo = chi >= clo ? clo : 128;
-      const unsigned vspan = chi >= clo ? (unsigned)(chi - clo) : 0u;
+      const int c0 = key0 + 64 * h;
       const uint32_t s_tm = tmem + lane_base + 128 * (J & 1) + 64 * h;
       f2 keep[32];
       ok = __all_sync(0xffffffffu, mbar_wait(&s_full[J & 1], (J / 2) & 1, kStatusTimeoutSoftmax));
@@ -795,16 +841,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
 #pragma unroll
         for (int c = 0; c < 16; ++c) row[c] = f2_pack(nlse, nlse);
         bwd_probs<kCap>(p, sv32, row, pr, fac);
-        if (need_mask) {
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const int col = 64 * h + 32 * g + 2 * c;
-            float a, b;
-            f2_unpack(pr[c], a, b);
-            pr[c] = f2_pack((unsigned)(col - vlo) > vspan ? 0.f : a,
-                            (unsigned)(col + 1 - vlo) > vspan ? 0.f : b);
-          }
-        }
+        if (need_mask) bwd_hide(pr, bwd_bits(lo - c0 - 32 * g, hi - c0 - 32 * g));
 #pragma unroll
         for (int c = 0; c < 16; ++c) keep[16 * g + c] = kCap ? f2_mul(pr[c], fac[c]) : pr[c];
       };
@@ -833,6 +870,8 @@ __global__ void __launch_bounds__(kBwThreads, 1)
       if (lane == 0) mbar_arrive(&ds_full[J & 1]);
     }
     if (!ok) break;
+    const int next = bwd_item(s, kk);
+    const Item next_it = item_at(next);  // ahead of the wait: divisions
     if (it.kr.t_count > 0) {
       ok = __all_sync(0xffffffffu, mbar_wait(o_done, busy & 1, kStatusTimeoutEpilogue));
       if (!ok) break;
@@ -840,10 +879,17 @@ __global__ void __launch_bounds__(kBwThreads, 1)
       tc_fence_after();
     }
     // Each warpgroup stores its half of the columns.
-    if (quarter * 32 < it.nr)
-      bwd_store_row(p.dq + ((long long)it.run * s.run + it.r0 + r) * s.head_dim, tmem + lane_base + 384,
-                    64 * h, min(64 * h + 64, d_pad), s.head_dim, p.scale, it.kr.t_count == 0, r < it.nr);
+    if (quarter * 32 < it.nr && 64 * h < s.head_dim)
+      bwd_store_box(&tm_dq, smem + C::kStage + (warp - 4) * 4096, tmem + lane_base + 384 + 64 * h,
+                    64 * h, it.r0 + quarter * 32, it.run, p.scale, it.kr.t_count == 0, false, lane);
+    if (lane == 0) {
+      bulk_wait_read();  // the box goes back to the loader, or to the next item
+      if (it.kr.t_count > 0) mbar_arrive(do_empty);
     }
+    i = next;
+    it = next_it;
+    }
+    if (lane == 0) bulk_wait_all();  // stores done before the CTA exits
   }
   tc_fence_before();
   __syncthreads();

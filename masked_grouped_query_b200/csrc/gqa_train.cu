@@ -122,22 +122,25 @@ int launch_bwd_sm100(const BwdParams& p, int device, int sms, cudaStream_t st) {
   if (rc == GQA_ATTN_OK) rc = bwd_sm100_setup(bwd_dq_kernel<DCH, kCap>, C::kSmemBytes, device, done_q);
   if (rc != GQA_ATTN_OK) return rc;
   const BwdShape& s = p.sh;
-  CUtensorMap q, dout, k, v;
+  CUtensorMap q, dout, k, v, dq, dk, dv;
   const struct {
     CUtensorMap* map;
     const void* base;
     bool rows;
-  } maps[4] = {{&q, p.q, true}, {&dout, p.dout, true}, {&k, p.k, false}, {&v, p.v, false}};
+    int box;
+  } maps[7] = {{&q, p.q, true, 128},  {&dout, p.dout, true, 128}, {&k, p.k, false, 128},
+               {&v, p.v, false, 128}, {&dq, p.dq, true, 32},      {&dk, p.dk, false, 32},
+               {&dv, p.dv, false, 32}};
   for (const auto& m : maps)
     if ((rc = gqa_host::tensor_map(m.map, m.base, s.head_dim, m.rows ? s.run : s.kv_len,
-                                   m.rows ? s.runs : s.units, 128)) != GQA_ATTN_OK)
+                                   m.rows ? s.runs : s.units, m.box)) != GQA_ATTN_OK)
       return rc;
   const long long key_tiles = s.units * ceil_div(s.kv_len, 128), row_tiles = s.runs * s.tiles;
   const unsigned kv_grid = (unsigned)(key_tiles < sms ? key_tiles : sms);
-  bwd_dkdv_kernel<DCH, kCap><<<kv_grid, kBwThreads, C::kSmemBytes, st>>>(q, dout, k, v, p);
+  bwd_dkdv_kernel<DCH, kCap><<<kv_grid, kBwThreads, C::kSmemBytes, st>>>(q, dout, k, v, dk, dv, p);
   if ((rc = launched("launch(backward dK dV)")) != GQA_ATTN_OK) return rc;
   const unsigned q_grid = (unsigned)(row_tiles < sms ? row_tiles : sms);
-  bwd_dq_kernel<DCH, kCap><<<q_grid, kBwThreads, C::kSmemBytes, st>>>(q, dout, k, v, p);
+  bwd_dq_kernel<DCH, kCap><<<q_grid, kBwThreads, C::kSmemBytes, st>>>(q, dout, k, v, dq, p);
   return launched("launch(backward dQ)");
 }
 
