@@ -249,11 +249,8 @@ int gqa_attn_bwd(const void* dout, const void* q, const void* k, const void* v, 
   p.logit_scale = kLog2e32 * p.scale;
   p.cap_in = p.softcap ? p.scale / softcap : 0.f;
   p.cap_out = p.softcap ? softcap * kLog2e32 : 0.f;
-  // Statistics: 16 rows a block, at most eight blocks (2048 threads) per SM.
-  const long long want = s.runs * s.tiles * 8;
-  const long long blocks = want < 8LL * sms ? want : 8LL * sms;
-  bwd_stats_kernel<<<(unsigned)blocks, 256, 0, st>>>(p.dout, (const __nv_bfloat16*)o, lse, dlse,
-                                                     (float*)scratch, s);
+  bwd_stats_kernel<<<(unsigned)(s.runs * s.tiles), kBwStatThreads, 0, st>>>(
+      p.dout, (const __nv_bfloat16*)o, lse, dlse, (float*)scratch, s);
   if ((rc = launched("launch(backward statistics)")) != GQA_ATTN_OK) return rc;
   // The tcgen05 kernels hold dK and dV of 128 columns each in TMEM next to the
   // scores: wider heads stay on mma.sync (force_path 1 does for every width).

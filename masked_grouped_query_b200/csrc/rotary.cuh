@@ -43,41 +43,25 @@ struct RotaryParams {
   unsigned char axis[kRotMaxPairs];
 };
 
+// V elements as they lie in memory (one access), and as floats.
 template <typename T, int V>
-struct RotVec;
-template <int V>
-struct __align__(2 * V) RotBf {
-  __nv_bfloat16 x[V];
+struct __align__(sizeof(T) * V > 16 ? 16 : sizeof(T) * V) RotVec {
+  T x[V];
 };
-template <int V>
-struct __align__(V >= 4 ? 16 : 4 * V) RotF {
-  float x[V];
-};
-template <int V>
-__device__ __forceinline__ void rot_load(const __nv_bfloat16* p, float (&f)[V]) {
-  const RotBf<V> v = *reinterpret_cast<const RotBf<V>*>(p);
+__device__ __forceinline__ float rot_float(float x) { return x; }
+__device__ __forceinline__ float rot_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T rot_round(float x);
+template <>
+__device__ __forceinline__ float rot_round<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 rot_round<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+template <typename T, int V>
+__device__ __forceinline__ void rot_store(T* p, const float (&f)[V]) {
+  RotVec<T, V> v;
 #pragma unroll
-  for (int i = 0; i < V; ++i) f[i] = __bfloat162float(v.x[i]);
-}
-template <int V>
-__device__ __forceinline__ void rot_load(const float* p, float (&f)[V]) {
-  const RotF<V> v = *reinterpret_cast<const RotF<V>*>(p);
-#pragma unroll
-  for (int i = 0; i < V; ++i) f[i] = v.x[i];
-}
-template <int V>
-__device__ __forceinline__ void rot_store(__nv_bfloat16* p, const float (&f)[V]) {
-  RotBf<V> v;
-#pragma unroll
-  for (int i = 0; i < V; ++i) v.x[i] = __float2bfloat16_rn(f[i]);
-  *reinterpret_cast<RotBf<V>*>(p) = v;
-}
-template <int V>
-__device__ __forceinline__ void rot_store(float* p, const float (&f)[V]) {
-  RotF<V> v;
-#pragma unroll
-  for (int i = 0; i < V; ++i) v.x[i] = f[i];
-  *reinterpret_cast<RotF<V>*>(p) = v;
+  for (int i = 0; i < V; ++i) v.x[i] = rot_round<T>(f[i]);
+  *reinterpret_cast<RotVec<T, V>*>(p) = v;
 }
 
 template <int V, typename TI, typename TO, bool kInterleaved>
@@ -109,37 +93,42 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
   } else {
     off0 = off1 = 2 * p.pairs + (vec * V - p.pairs);
   }
-  constexpr int U = 4;  // heads in flight per thread
-  for (int hb = h0; hb < h1; hb += U) {
-    float x[U][V], z[U][V];
+  // Heads in flight per thread: their vectors stay as loaded until they are
+  // turned, 16 or 32 bytes a head.
+  constexpr int U = sizeof(TI) * V >= 16 ? 4 : 8;
+  // A batch of heads lies in q or in k, never across.
+  for (int hb = h0; hb < h1;) {
+    const int w = hb >= p.q_heads;
+    const int base = w ? p.q_heads : 0, end = w ? h1 : min(h1, p.q_heads);
+    const int n = min(U, end - hb);
+    const TI* src = static_cast<const TI*>(w ? p.k : p.q) + b * p.in_b[w] +
+                    (hb - base) * p.in_h[w] + l * p.in_l[w];
+    TO* dst = static_cast<TO*>(w ? p.k_out : p.q_out) + b * p.out_b[w] + (hb - base) * p.out_h[w] +
+              l * p.out_l[w];
+    const long long ih = p.in_h[w], oh = p.out_h[w];
+    RotVec<TI, V> x[U], z[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = hb + u;
-      if (h >= h1) break;
-      const int w = h >= p.q_heads;
-      const TI* src = static_cast<const TI*>(w ? p.k : p.q) + b * p.in_b[w] +
-                      (h - (w ? p.q_heads : 0)) * p.in_h[w] + l * p.in_l[w];
-      rot_load<V>(src + off0, x[u]);
-      if (turns) rot_load<V>(src + off1, z[u]);
+      if (u >= n) break;
+      x[u] = *reinterpret_cast<const RotVec<TI, V>*>(src + u * ih + off0);
+      if (turns) z[u] = *reinterpret_cast<const RotVec<TI, V>*>(src + u * ih + off1);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = hb + u;
-      if (h >= h1) break;
-      const int w = h >= p.q_heads;
-      TO* dst = static_cast<TO*>(w ? p.k_out : p.q_out) + b * p.out_b[w] +
-                (h - (w ? p.q_heads : 0)) * p.out_h[w] + l * p.out_l[w];
+      if (u >= n) break;
+      float a[V], c[V];
       if (!turns) {
-        rot_store<V>(dst + off0, x[u]);
+#pragma unroll
+        for (int i = 0; i < V; ++i) a[i] = rot_float(x[u].x[i]);
+        rot_store<TO, V>(dst + u * oh + off0, a);
         continue;
       }
-      float a[V], c[V];
       if constexpr (kInterleaved) {
         // The 2 V elements x | z hold pairs (0, 1), (2, 3), ...
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const float e = 2 * i < V ? x[u][2 * i % V] : z[u][2 * i % V];
-          const float f = 2 * i + 1 < V ? x[u][(2 * i + 1) % V] : z[u][(2 * i + 1) % V];
+          const float e = rot_float(2 * i < V ? x[u].x[2 * i % V] : z[u].x[2 * i % V]);
+          const float f = rot_float(2 * i + 1 < V ? x[u].x[(2 * i + 1) % V] : z[u].x[(2 * i + 1) % V]);
           const float re = e * cs[i] - f * sn[i], im = f * cs[i] + e * sn[i];
           if (2 * i < V) a[2 * i % V] = re; else c[2 * i % V] = re;
           if (2 * i + 1 < V) a[(2 * i + 1) % V] = im; else c[(2 * i + 1) % V] = im;
@@ -147,13 +136,15 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
       } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          a[i] = x[u][i] * cs[i] - z[u][i] * sn[i];
-          c[i] = z[u][i] * cs[i] + x[u][i] * sn[i];
+          const float e = rot_float(x[u].x[i]), f = rot_float(z[u].x[i]);
+          a[i] = e * cs[i] - f * sn[i];
+          c[i] = f * cs[i] + e * sn[i];
         }
       }
-      rot_store<V>(dst + off0, a);
-      rot_store<V>(dst + off1, c);
+      rot_store<TO, V>(dst + u * oh + off0, a);
+      rot_store<TO, V>(dst + u * oh + off1, c);
     }
+    hb += n;
   }
 }
 
