@@ -347,10 +347,11 @@ int gqa_attn_rotary(const void* q, const void* k, void* q_out, void* k_out, cons
   // 4 elements when the pairs divide by it, else single elements.
   const int v = pairs % 8 == 0 && !in32 && !out32 && !interleaved ? 8 : pairs % 4 == 0 ? 4 : 1;
   p.vecs = ((int)pairs + (head_dim - 2 * (int)pairs)) / v;
-  // All heads of a token in one thread, unless that leaves the SMs short of
-  // threads: then runs of heads, down to a single one.
+  // All heads of a token in one thread, unless that leaves an SM with less
+  // than its 2048 threads: then runs of heads, down to a single one.  (At 1024
+  // or 4096 threads the measured cases take up to 10% longer.)
   const long long threads = tokens * p.vecs;
-  const long long runs = ceil_div((long long)sms * 1024, threads);
+  const long long runs = ceil_div((long long)sms * 2048, threads);
   p.heads_per_thread = (int)(runs >= heads ? 1 : ceil_div(heads, runs));
   const long long gx = ceil_div(threads, kRotThreads);
   if (gx > 0x7fffffffLL) return GQA_ATTN_ERR_TOO_LARGE;
