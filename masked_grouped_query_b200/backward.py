@@ -15,7 +15,21 @@ import ctypes
 import torch
 
 from . import _lib
-from .attention import _args, _check_tensor, _stream_handle
+from .attention import _args, _check_tensor
+
+
+def _stream_of(stream, device) -> int:
+    """The cudaStream_t of ``stream``, or of ``device``'s current stream."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream.cuda_stream
+
+
+def _device(device):
+    """``device`` as the current one; entering it costs more than asking."""
+    if torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
 
 
 def _on(stream):
@@ -70,10 +84,10 @@ def attention_lse(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: 
         else:
             _check_rows("lse", lse, q)
     lib = _lib.load()
-    with torch.cuda.device(q.device):
+    with _device(q.device):
         rc = lib.gqa_attn_fwd_lse(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                                   lse.data_ptr(), *dims, *_args(window, softcap, causal),
-                                  _stream_handle(stream))
+                                  _stream_of(stream, q.device))
     _lib.check(rc, "gqa_attn_fwd_lse")
     return out, lse
 
@@ -106,11 +120,11 @@ def attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
                 _check_like(n, t, like)
             outs.append(t)
         scratch = torch.empty(size.value, dtype=torch.uint8, device=q.device)
-    with torch.cuda.device(q.device):
+    with _device(q.device):
         rc = lib.gqa_attn_bwd(do.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
                               o.data_ptr(), lse.data_ptr(),
                               None if dlse is None else dlse.data_ptr(),
                               *[t.data_ptr() for t in outs], scratch.data_ptr(), size.value,
-                              *dims, c, w, s, _stream_handle(stream))
+                              *dims, c, w, s, _stream_of(stream, q.device))
     _lib.check(rc, "gqa_attn_bwd")
     return tuple(outs)

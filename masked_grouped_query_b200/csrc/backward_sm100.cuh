@@ -31,6 +31,14 @@
 // P is recomputed as 2^(x - lse) with both in log2 units: the statistics are
 // known, so there is no running maximum and nothing to rescale.  The fp32 P
 // stays in registers between the two elementwise halves of a tile.
+//
+// The dQ kernel does not wait for the other one: both need the statistics
+// alone.  Each launch may start when the kernel before it has started
+// everywhere, so on small problems the two run side by side, and on large ones
+// dQ's CTAs take each SM as it becomes free.  The chain: the dK/dV kernel
+// waits for the statistics, then lets dQ's CTAs start (the statistics are
+// therefore complete for them too); every dQ CTA waits for the dK/dV kernel
+// before it ends, so that whatever follows in the stream finds both done.
 // All waits are bounded.
 #pragma once
 
@@ -325,6 +333,10 @@ __global__ void __launch_bounds__(kBwThreads, 1)
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
+  }
+  if (threadIdx.x == 0) {
+    grid_wait();
+    grid_launch_dependents();
   }
   tc_fence_before();
   __syncthreads();
@@ -891,6 +903,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
     }
     if (lane == 0) bulk_wait_all();  // stores done before the CTA exits
   }
+  if (threadIdx.x == 0) grid_wait();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

@@ -4,7 +4,8 @@ The prefill softmax applies the logit softcap s * tanh(x / s).  When every
 |x / s| of a warp's tile is at most 1/2 (the common case: logits far below
 the cap) it evaluates tanh(y) ~= y * P(y^2) with P of 4 terms (degree 7,
 kTanhC*) or, for caps up to kTanh5MaxCap, 3 terms (degree 5, kTanh5C*); the
-paths that return row statistics in fp32 take 5 terms (degree 9, kTanh9C*).
+paths that return row statistics in fp32 take 7 terms on [0, 1] (degree 13,
+kTanh13C*).
 Fitted here for least maximum absolute error on [0, 1/2] (linear
 programming on a grid); otherwise it uses the hardware tanh.  Run:
     python masked_grouped_query_b200/csrc/fit_tanh_poly.py
@@ -28,8 +29,8 @@ def fit(terms=4, n=4001, ymax=0.5):
 
 
 if __name__ == "__main__":
-    for terms in (5, 4, 3):
-        c, e = fit(terms=terms)
+    for terms, ymax in ((7, 1.0), (4, 0.5), (3, 0.5)):
+        c, e = fit(terms=terms, ymax=ymax)
         print(f"degree {2 * terms - 1}:")
         for k, v in enumerate(c):
             print(f"  c{2 * k + 1} = {np.float32(v).item()!r}f")

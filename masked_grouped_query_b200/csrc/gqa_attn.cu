@@ -42,7 +42,7 @@ struct DeviceInfo {
   int sms = 0, major = 0, minor = 0;
   int smem_optin = 0;
   bool decode_attr[20] = {};  // per instantiation: [0, 8) 3/2-stage, [8, 10) 5-stage; + 10 with lse
-  bool prefill_attr[32] = {};  // per (DCH, softcap code, split mode) instantiation; [24, 32) with lse
+  bool prefill_attr[36] = {};  // per (DCH, softcap code, split mode) instantiation; [24, 36) with lse
   int append_blocks[4] = {};    // resident kv_append blocks per SM, per instantiation
   bool append_runs_ready[4] = {};  // staged-runs kernel's smem attribute set
   // Clusters of n CTAs of a split instantiation that can be resident at once
@@ -531,12 +531,12 @@ float cap_base_offset(float cap_out) { return std::max(16.0f, 2.0f * cap_out - 1
 // tanh polynomial with a fixed exponent base (no row max; caps up to about
 // 63.8); 5 = the degree-5 polynomial with the row max (caps up to
 // kTanh5MaxCap, or any cap when override key 5 asks for it); 7 = degree 7.
-// With row statistics wanted: always 7 (the kLse kernels put degree 9 there).
+// With row statistics wanted: 3 or 7 (the kLse kernels put degree 13 there).
 int cap_degree(const Problem& pr) {
   if (!(pr.softcap > 0.f)) return 0;
-  if (pr.lse) return 7;
-  if (pr.softcap > kTanh5MaxCap) return 7;
   const bool fixed = cap_base_offset(pr.softcap * kLog2e) <= 64.0f && g_force_two_pass.load() == 0;
+  if (pr.lse) return fixed ? 3 : 7;
+  if (pr.softcap > kTanh5MaxCap) return 7;
   return fixed ? 3 : 5;
 }
 
@@ -544,7 +544,7 @@ int cap_degree(const Problem& pr) {
 // 2 = paired splits merged inside a cluster.
 template <int DCH, int kCapDeg, int kSplit, bool kLse = false>
 constexpr int prefill_slot() {
-  if (kLse) return 24 + (DCH - 1) + 2 * (kCapDeg == 7 ? 1 : 0) + 4 * kSplit;
+  if (kLse) return 24 + (DCH - 1) + 2 * (kCapDeg == 7 ? 2 : kCapDeg == 3 ? 1 : 0) + 6 * kSplit;
   return (DCH - 1) + 2 * (kCapDeg == 5 ? 1 : kCapDeg == 7 ? 2 : kCapDeg == 3 ? 3 : 0) +
          8 * kSplit;
 }
@@ -717,10 +717,12 @@ int launch_prefill(const Problem& pr, const Plan& pl, DeviceInfo& dev, int csize
     auto go = [&](auto fn) { return fn(pr, pl, dev, 0, q, k, v, o, ws, tickets, stream); };
     const bool split = pl.splits > 1;
     if (pl.dch == 1)
-      return deg ? go(split ? launch_prefill_k<1, 7, 1, true> : launch_prefill_k<1, 7, 0, true>)
-                 : go(split ? launch_prefill_k<1, 0, 1, true> : launch_prefill_k<1, 0, 0, true>);
-    return deg ? go(split ? launch_prefill_k<2, 7, 1, true> : launch_prefill_k<2, 7, 0, true>)
-               : go(split ? launch_prefill_k<2, 0, 1, true> : launch_prefill_k<2, 0, 0, true>);
+      return deg == 7   ? go(split ? launch_prefill_k<1, 7, 1, true> : launch_prefill_k<1, 7, 0, true>)
+             : deg == 3 ? go(split ? launch_prefill_k<1, 3, 1, true> : launch_prefill_k<1, 3, 0, true>)
+                        : go(split ? launch_prefill_k<1, 0, 1, true> : launch_prefill_k<1, 0, 0, true>);
+    return deg == 7   ? go(split ? launch_prefill_k<2, 7, 1, true> : launch_prefill_k<2, 7, 0, true>)
+           : deg == 3 ? go(split ? launch_prefill_k<2, 3, 1, true> : launch_prefill_k<2, 3, 0, true>)
+                      : go(split ? launch_prefill_k<2, 0, 1, true> : launch_prefill_k<2, 0, 0, true>);
   }
   if (pl.dch == 1)
     return deg == 3 ? launch_prefill_d<1, 3>(pr, pl, dev, csize, q, k, v, o, ws, tickets, stream)

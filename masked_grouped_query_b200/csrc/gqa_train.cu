@@ -114,6 +114,25 @@ int bwd_sm100_setup(K kernel, int bytes, int device, bool* done) {
   return allow_smem(kernel, bytes, device, done);
 }
 
+// A launch that may start before the kernel ahead of it in the stream ends
+// (see the head of backward_sm100.cuh).
+template <typename... P, typename... A>
+int launch_after(const char* where, void (*kernel)(P...), long long grid, int threads, int smem,
+                 cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  return e == cudaSuccess ? GQA_ATTN_OK : cuda_fail(where, e, GQA_ATTN_ERR_LAUNCH);
+}
+
 template <int DCH, bool kCap>
 int launch_bwd_sm100(const BwdParams& p, int device, int sms, cudaStream_t st) {
   using C = BwdCfg<DCH>;
@@ -136,12 +155,15 @@ int launch_bwd_sm100(const BwdParams& p, int device, int sms, cudaStream_t st) {
                                    m.rows ? s.runs : s.units, m.box)) != GQA_ATTN_OK)
       return rc;
   const long long key_tiles = s.units * ceil_div(s.kv_len, 128), row_tiles = s.runs * s.tiles;
-  const unsigned kv_grid = (unsigned)(key_tiles < sms ? key_tiles : sms);
-  bwd_dkdv_kernel<DCH, kCap><<<kv_grid, kBwThreads, C::kSmemBytes, st>>>(q, dout, k, v, dk, dv, p);
-  if ((rc = launched("launch(backward dK dV)")) != GQA_ATTN_OK) return rc;
-  const unsigned q_grid = (unsigned)(row_tiles < sms ? row_tiles : sms);
-  bwd_dq_kernel<DCH, kCap><<<q_grid, kBwThreads, C::kSmemBytes, st>>>(q, dout, k, v, dq, p);
-  return launched("launch(backward dQ)");
+  if ((rc = launch_after("launch(backward dK dV)", bwd_dkdv_kernel<DCH, kCap>,
+                         key_tiles < sms ? key_tiles : sms, kBwThreads, C::kSmemBytes, st, q, dout, k,
+                         v, dk, dv, p)) != GQA_ATTN_OK)
+    return rc;
+  // Four CTAs per SM, one after the other, even out what the key tiles left
+  // uneven (one SM's share at a time would keep it).
+  const long long q_grid = row_tiles < 4LL * sms ? row_tiles : 4LL * sms;
+  return launch_after("launch(backward dQ)", bwd_dq_kernel<DCH, kCap>, q_grid, kBwThreads,
+                      C::kSmemBytes, st, q, dout, k, v, dq, p);
 }
 
 // ------------------------------------------------------------------ rotary
@@ -335,14 +357,21 @@ int gqa_attn_rotary(const void* q, const void* k, void* q_out, void* k_out, cons
   }
   // Frequency of pair i: theta^(-i / pairs), or theta^(-j / section) for the
   // j-th pair of its axis, as turns per position.
+  // One power a step: the products' rounding grows by 2^-53 a pair.
   const double pi2 = 6.283185307179586476925286766559;
+  const bool per_axis = flags & GQA_ROTARY_PER_AXIS;
+  double ratio = std::pow(theta, -1.0 / (double)pairs), f = 1.0;
   int at = 0;
-  for (int a = 0; a < num_axes; ++a)
-    for (int j = 0; j < sections[a]; ++j, ++at) {
-      const double e = (flags & GQA_ROTARY_PER_AXIS) ? (double)j / sections[a] : (double)at / (double)pairs;
-      p.turn[at] = std::pow(theta, -e) / pi2;
+  for (int a = 0; a < num_axes; ++a) {
+    if (per_axis) {
+      ratio = std::pow(theta, -1.0 / sections[a]);
+      f = 1.0;
+    }
+    for (int j = 0; j < sections[a]; ++j, ++at, f *= ratio) {
+      p.turn[at] = f / pi2;
       p.axis[at] = (unsigned char)a;
     }
+  }
   // The widest vector that keeps every access aligned: 8 bf16 (16 bytes) or
   // 4 elements when the pairs divide by it, else single elements.
   const int v = pairs % 8 == 0 && !in32 && !out32 && !interleaved ? 8 : pairs % 4 == 0 ? 4 : 1;

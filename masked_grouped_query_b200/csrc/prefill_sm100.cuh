@@ -122,6 +122,25 @@ __device__ __forceinline__ float row_lse(float m, float l) {
   return l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
+// cap_out * tanh(x * cap_in) + c for a pair with |x * cap_in| <= 1, as x Q(x^2)
+// with the scales folded into the degree-13 polynomial's coefficients.
+struct LogitPoly13 {
+  f2 q[7];
+  __device__ __forceinline__ LogitPoly13(float cap_in, float cap_out) {
+    const float k[7] = {kTanh13C1, kTanh13C3, kTanh13C5, kTanh13C7, kTanh13C9, kTanh13C11, kTanh13C13};
+    float f = cap_in * cap_out;
+#pragma unroll
+    for (int i = 0; i < 7; ++i, f *= cap_in * cap_in) q[i] = f2_pack(f * k[i], f * k[i]);
+  }
+  __device__ __forceinline__ f2 operator()(f2 x, f2 c) const {
+    const f2 x2 = f2_mul(x, x);
+    f2 r = q[6];
+#pragma unroll
+    for (int i = 5; i >= 0; --i) r = f2_fma(r, x2, q[i]);
+    return f2_fma(x, r, c);
+  }
+};
+
 template <int DCH>
 struct PrefillCfg {
   static constexpr int kBoxBytes = 128 * 128;            // 128 rows x 64 bf16
@@ -309,8 +328,8 @@ __device__ __forceinline__ int key_tile(const PfItem& it, int t, int j) {
 // returns every row's log-sum-exp in fp32.  Those kernels spend what the
 // others save at an error below the bf16 output's rounding: every 2^x on
 // MUFU (2^-22 relative; the FMA-pipe cubic has 7.5e-5) and an accurate tanh
-// (degree 9, or 1 - 2 / (1 + e^2y)).  They exist with kCapDeg 0 and 7 only,
-// and merge splits by ticket.
+// (degree 13 up to 1, or 1 - 2 / (1 + e^2y)).  They exist with kCapDeg 0, 3
+// (fixed base) and 7 (row max) only, and merge splits by ticket.
 template <int DCH, int kCapDeg, int kSplit, bool kLse = false>
 __global__ void __launch_bounds__(kPfThreads, 1)
     prefill_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -712,14 +731,30 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll
               for (int c = 2; c < 32; c += 2)
                 am = fmax3(am, fabsf(__uint_as_float(sv[c])), fabsf(__uint_as_float(sv[c + 1])));
-              const bool poly = __all_sync(0xffffffffu, am * p.cap_in <= 0.5f);
+              const bool poly = __all_sync(0xffffffffu, am * p.cap_in <= (kLse ? 1.f : 0.5f));
               if (need_mask) {
 #pragma unroll
                 for (int c = 0; c < 32; ++c)
                   if ((unsigned)(32 * g + c - vlo) > vspan) sv[c] = __float_as_uint(-INFINITY);
               }
               uint32_t pk[16];
-              if (poly) {
+              if (kLse && poly) {
+                const LogitPoly13 logit(p.cap_in, p.cap_out);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                  f2 pv = exp2_mufu_x2(
+                      logit(f2_pack(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1])), nb));
+                  if (need_mask) {  // (a hidden key went through the polynomial as -inf)
+                    float pa, pb;
+                    f2_unpack(pv, pa, pb);
+                    const int col = 32 * g + 2 * c;
+                    pv = f2_pack((unsigned)(col - vlo) > vspan ? 0.f : pa,
+                                 (unsigned)(col + 1 - vlo) > vspan ? 0.f : pb);
+                  }
+                  acc[c & 3] = f2_add(acc[c & 3], pv);
+                  pk[c] = pack_bf16_f2(pv);
+                }
+              } else if (poly) {
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
                   const f2 v = f2_pack(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1]));
@@ -733,8 +768,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
                   const float a = __uint_as_float(sv[2 * c]), b = __uint_as_float(sv[2 * c + 1]);
-                  f2 pv = exp2_mufu_x2(f2_pack(fmaf(co, tanh_fast(a * ci), -base),
-                                               fmaf(co, tanh_fast(b * ci), -base)));
+                  f2 pv = kLse ? exp2_mufu_x2(f2_pack(fmaf(co, tanh_large(a * ci), -base),
+                                                      fmaf(co, tanh_large(b * ci), -base)))
+                               : exp2_mufu_x2(f2_pack(fmaf(co, tanh_fast(a * ci), -base),
+                                                      fmaf(co, tanh_fast(b * ci), -base)));
                   if (need_mask) {
                     float pa, pb;
                     f2_unpack(pv, pa, pb);
@@ -810,7 +847,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             mraw = fmax3(mraw, m2[0], m2[1]);
           }
           if (need_mask) tmem_st_wait();  // pass 2 reads the masked scores
-          if constexpr (kCap) small_y = __all_sync(0xffffffffu, amax * p.cap_in <= 0.5f);
+          if constexpr (kCap) small_y = __all_sync(0xffffffffu, amax * p.cap_in <= (kLse ? 1.f : 0.5f));
         }
         const float mt = mraw == -INFINITY ? -INFINITY
                          : kCap ? p.cap_out * tanh_fast(mraw * p.cap_in)
@@ -906,17 +943,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               return f2_fma(v, f2_fma(f2_fma(q2, v2, q1), v2, q0), nb);
             }, No());
           } else if constexpr (kLse) {
-            const f2 q0 = f2_pack(cc * kTanh9C1, cc * kTanh9C1);
-            const f2 q1 = f2_pack(cc * ci2 * kTanh9C3, cc * ci2 * kTanh9C3);
-            const f2 q2 = f2_pack(cc * ci2 * ci2 * kTanh9C5, cc * ci2 * ci2 * kTanh9C5);
-            const float ci6 = ci2 * ci2 * ci2;
-            const f2 q3 = f2_pack(cc * ci6 * kTanh9C7, cc * ci6 * kTanh9C7);
-            const f2 q4 = f2_pack(cc * ci6 * ci2 * kTanh9C9, cc * ci6 * ci2 * kTanh9C9);
-            emit([&](f2 v) {
-              const f2 v2 = f2_mul(v, v);
-              return f2_fma(
-                  v, f2_fma(f2_fma(f2_fma(f2_fma(q4, v2, q3), v2, q2), v2, q1), v2, q0), nb);
-            }, Yes());
+            const LogitPoly13 poly(p.cap_in, p.cap_out);
+            emit([&](f2 v) { return poly(v, nb); }, Yes());
           } else {
             const f2 q0 = f2_pack(cc * kTanhC1, cc * kTanhC1);
             const f2 q1 = f2_pack(cc * ci2 * kTanhC3, cc * ci2 * kTanhC3);
@@ -934,8 +962,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             float a, b;
             f2_unpack(v, a, b);
             if constexpr (kLse)
-              return f2_pack(fmaf(co, tanh_accurate(a * ci), -base),
-                             fmaf(co, tanh_accurate(b * ci), -base));
+              return f2_pack(fmaf(co, tanh_large(a * ci), -base),
+                             fmaf(co, tanh_large(b * ci), -base));
             return f2_pack(fmaf(co, tanh_fast(a * ci), -base), fmaf(co, tanh_fast(b * ci), -base));
           }, Yes());
         }

@@ -13,8 +13,7 @@ import ctypes
 import torch
 
 from . import _lib
-from .attention import _stream_handle
-from .backward import _on
+from .backward import _device, _on, _stream_of
 
 IN_SEQ_MAJOR = 0x1
 OUT_SEQ_MAJOR = 0x2
@@ -102,9 +101,9 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, *, 
              | (INTERLEAVED if interleaved else 0) | (PER_AXIS if per_axis else 0)
              | (INVERSE if inverse else 0))
     ptr = [None if t is None else t.data_ptr() for t in (q, k, *outs)]
-    with torch.cuda.device(q.device):
+    with _device(q.device):
         rc = _lib.load().gqa_attn_rotary(*ptr, positions.data_ptr(), b, length, hq, hkv, d,
                                          len(sections), (ctypes.c_int * len(sections))(*sections),
-                                         float(theta), flags, _stream_handle(stream))
+                                         float(theta), flags, _stream_of(stream, q.device))
     _lib.check(rc, "gqa_attn_rotary")
     return tuple(outs)
