@@ -157,11 +157,13 @@ __global__ void __launch_bounds__(kBwStatThreads)
 }
 
 // ------------------------------------------------------------------ mma.sync
-// The plain form of both kernels: 64 x 64 tiles on mma.sync m16n8k16.  It
-// takes every head_dim up to 256; the tcgen05 kernels take over up to 128.
+// Both kernels as 64 x 64 tiles on mma.sync m16n8k16, for every head_dim up
+// to 256; the tcgen05 kernels take over up to 128 (with wider heads their
+// accumulators alone would fill TMEM, and two operand tiles shared memory).
 //
 // One CTA keeps the 64 rows of its own two operands in shared memory (K, V
-// for dK/dV; Q, dO for dQ) and streams 64-row tiles of the other two.  Eight
+// for dK/dV; Q, dO for dQ) and streams 64-row tiles of the other two through
+// two buffers (cp.async: the next tiles load under this one's products).  Eight
 // warps: warp w computes the 16 x 32 piece (16 own rows from w % 4, 32
 // streamed rows from w / 4) of S and dP, leaves P and dS as bf16 in shared
 // memory, and accumulates 16 own rows x half of the columns of its outputs in
@@ -174,19 +176,20 @@ struct BwdMmaCfg {
   static constexpr int kPitch = KS * 16 + 8;  // elements: rows 16 bytes off a multiple of 128
   static constexpr int kTileElems = kBmTile * kPitch;
   static constexpr int kPPitch = kBmTile + 8;
-  static constexpr int kSmemBytes = (4 * kTileElems + 2 * kBmTile * kPPitch) * 2 + 2 * kBmTile * 4;
+  static constexpr int kSmemBytes = (6 * kTileElems + 2 * kBmTile * kPPitch) * 2 + 4 * kBmTile * 4;
 };
 
-// rows [r0, r0 + n) x D of a [rows][D] matrix into a padded tile, zeros elsewhere.
+// n rows x D of a [rows][D] matrix into a padded tile, zeros elsewhere
+// (asynchronously: part of the thread's next committed group).
 template <int KS>
 __device__ __forceinline__ void bwd_load_tile(__nv_bfloat16* dst, const __nv_bfloat16* src, int D,
                                               int n) {
   using C = BwdMmaCfg<KS>;
+#pragma unroll 4
   for (int i = threadIdx.x; i < kBmTile * KS * 2; i += kBmThreads) {
     const int r = i / (KS * 2), c = (i - r * (KS * 2)) * 8;
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    if (r < n && c < D) x = *reinterpret_cast<const uint4*>(src + (long long)r * D + c);
-    *reinterpret_cast<uint4*>(dst + r * C::kPitch + c) = x;
+    const bool in = r < n && c < D;
+    cp_async16(dst + r * C::kPitch + c, in ? src + (long long)r * D + c : src, in);
   }
 }
 
@@ -197,11 +200,16 @@ __global__ void __launch_bounds__(kBmThreads, 1) bwd_mma_kernel(const BwdParams 
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __nv_bfloat16* own1 = (__nv_bfloat16*)smem_raw;  // K (dK/dV) or Q (dQ)
   __nv_bfloat16* own2 = own1 + C::kTileElems;      // V or dO
-  __nv_bfloat16* str1 = own2 + C::kTileElems;      // Q or K
-  __nv_bfloat16* str2 = str1 + C::kTileElems;      // dO or V
-  __nv_bfloat16* pm = str2 + C::kTileElems;        // P  [own row][streamed row]
+  __nv_bfloat16* str = own2 + C::kTileElems;       // two buffers of Q, dO or K, V
+  __nv_bfloat16* pm = str + 4 * C::kTileElems;     // P  [own row][streamed row]
   __nv_bfloat16* dm = pm + kBmTile * C::kPPitch;   // dS
-  float* st = (float*)(dm + kBmTile * C::kPPitch); // 64 times -lse, 64 delta of the query rows
+  float* st2 = (float*)(dm + kBmTile * C::kPPitch);  // two buffers: 64 times -lse, 64 delta of
+                                                     // the query rows
+  if (threadIdx.x == 0 && !kDQ) {  // the statistics; then dQ may start (see backward_sm100.cuh)
+    grid_wait();
+    grid_launch_dependents();
+  }
+  __syncthreads();
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t4 = lane & 3, mi = lane >> 3, rr = lane & 7;
@@ -242,22 +250,40 @@ __global__ void __launch_bounds__(kBmThreads, 1) bwd_mma_kernel(const BwdParams 
 #pragma unroll
   for (int i = 0; i < (kDQ ? 1 : KS); ++i) acc2[i][0] = acc2[i][1] = acc2[i][2] = acc2[i][3] = 0.f;
 
-  for (int it = 0; it < outer * count; ++it) {
+  // Tile `it` of the walk into its buffer.
+  auto fetch = [&](int it) {
     const long long run = run0 + (kDQ ? 0 : it / count);
-    const int str_row0 = (first + it % count) * kBmTile;
-    const int str_n = min(kBmTile, (kDQ ? s.kv_len : s.run) - str_row0);
-    __syncthreads();  // the previous tiles are no longer read
-    if (kDQ) {
-      bwd_load_tile<KS>(str1, p.k + (unit * s.kv_len + str_row0) * D, D, str_n);
-      bwd_load_tile<KS>(str2, p.v + (unit * s.kv_len + str_row0) * D, D, str_n);
-    } else {
-      bwd_load_tile<KS>(str1, p.q + (run * s.run + str_row0) * D, D, str_n);
-      bwd_load_tile<KS>(str2, p.dout + (run * s.run + str_row0) * D, D, str_n);
-    }
-    const int q_row0 = kDQ ? own_row0 : str_row0;
+    const int row0 = (first + it % count) * kBmTile;
+    const int n = min(kBmTile, (kDQ ? s.kv_len : s.run) - row0);
+    __nv_bfloat16* s1 = str + (it & 1) * 2 * C::kTileElems;
+    const long long off = (kDQ ? unit * s.kv_len + row0 : run * s.run + row0) * (long long)D;
+    bwd_load_tile<KS>(s1, (kDQ ? p.k : p.q) + off, D, n);
+    bwd_load_tile<KS>(s1 + C::kTileElems, (kDQ ? p.v : p.dout) + off, D, n);
     if (threadIdx.x < 128) {
-      const int w = threadIdx.x >> 6, r = threadIdx.x & 63;
-      st[threadIdx.x] = p.stats[(run * s.tiles + (q_row0 >> 7)) * 256 + w * 128 + (q_row0 & 127) + r];
+      const int w = threadIdx.x >> 6, r = threadIdx.x & 63, q_row0 = kDQ ? own_row0 : row0;
+      st2[(it & 1) * 128 + threadIdx.x] =
+          p.stats[(run * s.tiles + (q_row0 >> 7)) * 256 + w * 128 + (q_row0 & 127) + r];
+    }
+    cp_async_commit();
+  };
+  const int steps = outer * count;
+  if (steps > 0) {
+    fetch(0);
+  } else {  // never leave with copies in flight
+    cp_async_commit();
+    cp_async_wait<0>();
+  }
+  for (int it = 0; it < steps; ++it) {
+    const int str_row0 = (first + it % count) * kBmTile;
+    const int q_row0 = kDQ ? own_row0 : str_row0;
+    const __nv_bfloat16* str1 = str + (it & 1) * 2 * C::kTileElems;
+    const __nv_bfloat16* str2 = str1 + C::kTileElems;
+    const float* st = st2 + (it & 1) * 128;
+    if (it + 1 < steps) {  // its buffer was last read before the loop's closing barrier
+      fetch(it + 1);
+      cp_async_wait<1>();
+    } else {
+      cp_async_wait<0>();
     }
     __syncthreads();
 
@@ -344,6 +370,7 @@ __global__ void __launch_bounds__(kBmThreads, 1) bwd_mma_kernel(const BwdParams 
         }
       }
     }
+    __syncthreads();  // the buffer, P and dS are no longer read
   }
 
   const long long out0 = kDQ ? run0 * s.run + own_row0 : unit * s.kv_len + own_row0;
@@ -359,6 +386,7 @@ __global__ void __launch_bounds__(kBmThreads, 1) bwd_mma_kernel(const BwdParams 
       if constexpr (!kDQ)
         *(uint32_t*)(p.dv + off) = pack_bf16(acc2[n][2 * h], acc2[n][2 * h + 1]);
     }
+  if (kDQ && threadIdx.x == 0) grid_wait();
 }
 
 }  // namespace gqa

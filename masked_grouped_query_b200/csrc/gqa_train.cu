@@ -81,6 +81,25 @@ size_t bwd_scratch_bytes(const BwdShape& s) {
   return (size_t)s.runs * (size_t)s.tiles * 256 * sizeof(float);
 }
 
+// A launch that may start before the kernel ahead of it in the stream ends
+// (see the head of backward_sm100.cuh).
+template <typename... P, typename... A>
+int launch_after(const char* where, void (*kernel)(P...), long long grid, int threads, int smem,
+                 cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  return e == cudaSuccess ? GQA_ATTN_OK : cuda_fail(where, e, GQA_ATTN_ERR_LAUNCH);
+}
+
 template <int KS>
 int launch_bwd_mma(const BwdParams& p, int device, cudaStream_t st) {
   using C = BwdMmaCfg<KS>;
@@ -89,11 +108,12 @@ int launch_bwd_mma(const BwdParams& p, int device, cudaStream_t st) {
   if (rc == GQA_ATTN_OK) rc = allow_smem(bwd_mma_kernel<KS, true>, C::kSmemBytes, device, done_q);
   if (rc != GQA_ATTN_OK) return rc;
   const long long key_tiles = p.sh.units * ceil_div(p.sh.kv_len, kBmTile);
-  bwd_mma_kernel<KS, false><<<(unsigned)key_tiles, kBmThreads, C::kSmemBytes, st>>>(p);
-  if ((rc = launched("launch(backward dK dV)")) != GQA_ATTN_OK) return rc;
+  if ((rc = launch_after("launch(backward dK dV)", bwd_mma_kernel<KS, false>, key_tiles, kBmThreads,
+                         C::kSmemBytes, st, p)) != GQA_ATTN_OK)
+    return rc;
   const long long row_tiles = p.sh.runs * ceil_div(p.sh.run, kBmTile);
-  bwd_mma_kernel<KS, true><<<(unsigned)row_tiles, kBmThreads, C::kSmemBytes, st>>>(p);
-  return launched("launch(backward dQ)");
+  return launch_after("launch(backward dQ)", bwd_mma_kernel<KS, true>, row_tiles, kBmThreads,
+                      C::kSmemBytes, st, p);
 }
 
 // Shared memory limit of a tcgen05 backward kernel, and the check that its
@@ -112,25 +132,6 @@ int bwd_sm100_setup(K kernel, int bytes, int device, bool* done) {
     return detail(GQA_ATTN_ERR_LAUNCH, "backward kernel built with %d registers/thread: register "
                   "split needs %d", fa.numRegs, kBwRegTotal);
   return allow_smem(kernel, bytes, device, done);
-}
-
-// A launch that may start before the kernel ahead of it in the stream ends
-// (see the head of backward_sm100.cuh).
-template <typename... P, typename... A>
-int launch_after(const char* where, void (*kernel)(P...), long long grid, int threads, int smem,
-                 cudaStream_t st, const A&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = st;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  return e == cudaSuccess ? GQA_ATTN_OK : cuda_fail(where, e, GQA_ATTN_ERR_LAUNCH);
 }
 
 template <int DCH, bool kCap>
