@@ -65,10 +65,14 @@ struct BwdCfg {
   static constexpr int kBars = kStats + 2 * 1024;
   static constexpr int kNumBars = 26;
   // Output boxes, 4 KB for each of the eight elementwise warps: with 64
-  // columns there is room for them, with 128 they take the place of the
-  // resident operand of dP (V or dO), whose next load then waits for them.
-  static constexpr int kStage = DCH == 1 ? (kBars + kNumBars * 8 + 16 + 1023) / 1024 * 1024 : kTileBytes;
+  // columns there is room for them, with 128 they take the two-slot ring's
+  // slot of the item's last tile.  Its next load, the second tile of the next
+  // item, then waits for them; the first one does not.
+  static constexpr int kStage = (kBars + kNumBars * 8 + 16 + 1023) / 1024 * 1024;
   static constexpr int kSmemBytes = DCH == 1 ? kStage + 8 * 4096 : kBars + kNumBars * 8 + 16;
+  static __device__ __forceinline__ uint8_t* stage(uint8_t* smem, int last_tile) {
+    return DCH == 1 ? smem + kStage : smem + kRing2 + (last_tile & 1) * kTileBytes;
+  }
 };
 
 // Whether any row of a row tile fails to see any key of a key tile: only then
@@ -182,16 +186,16 @@ __device__ __forceinline__ void bwd_load32(const float* src, f2 (&v)[16]) {
 // leave these warps free meanwhile (from registers, in whole lines or not,
 // they took 1.5 to 2 times as long on the encoder shape).
 __device__ __forceinline__ void bwd_store_box(const CUtensorMap* map, uint8_t* stage, uint32_t tm,
-                                              int x, int row, int outer, float scale, bool zero,
-                                              bool again, int lane) {
+                                              int x, int row, int outer, float scale, bool again,
+                                              int lane) {
   uint32_t a[32], b[32], w[32];
   tmem_ld32(tm, a);
   tmem_ld32(tm + 32, b);
   tmem_ld_wait();
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
-    w[e] = zero ? 0u : pack_bf16(__uint_as_float(a[2 * e]) * scale, __uint_as_float(a[2 * e + 1]) * scale);
-    w[16 + e] = zero ? 0u : pack_bf16(__uint_as_float(b[2 * e]) * scale, __uint_as_float(b[2 * e + 1]) * scale);
+    w[e] = pack_bf16(__uint_as_float(a[2 * e]) * scale, __uint_as_float(a[2 * e + 1]) * scale);
+    w[16 + e] = pack_bf16(__uint_as_float(b[2 * e]) * scale, __uint_as_float(b[2 * e + 1]) * scale);
   }
   if (again) {
     if (lane == 0) bulk_wait_read();
@@ -207,6 +211,14 @@ __device__ __forceinline__ void bwd_store_box(const CUtensorMap* map, uint8_t* s
     tma_store_3d(map, stage, x, row, outer);
     bulk_commit();
   }
+}
+
+// Zeros for a warp's rows (contiguous in memory) of an item without a step.
+// Not through a box: the loader, which skips such items, may have filled it.
+__device__ __forceinline__ void bwd_store_zeros(__nv_bfloat16* dst, int rows, int head_dim, int lane) {
+  const int pieces = rows * (head_dim / 8);
+  for (int i = lane; i < pieces; i += 32)
+    reinterpret_cast<uint4*>(dst)[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
 // Bits lo..hi of a word (none when hi < lo, or outside 0..31).
@@ -310,14 +322,14 @@ __global__ void __launch_bounds__(kBwThreads, 1)
     mbar_init(k_empty, 1);
     mbar_init(drain, 2);
     mbar_init(v_full, 1);
-    mbar_init(v_empty, 1 + 8);  // the last dP^T, and the output boxes
+    mbar_init(v_empty, 1);
     for (int i = 0; i < 3; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&do_full[i], 1);
-      mbar_init(&do_empty[i], 2);  // both issuers
+      mbar_init(&do_empty[i], 2 + 8);  // both issuers, the elementwise warps
       mbar_init(&st_full[i], 1);
       mbar_init(&st_empty[i], 8);
     }
@@ -361,8 +373,8 @@ __global__ void __launch_bounds__(kBwThreads, 1)
 
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBwRegsLow));
   if (warp == 0 || warp == 3) {
-    // Two loaders: warp 0 K, Q and the statistics, warp 3 V and dO (V waits
-    // for the output boxes).
+    // Two loaders: warp 0 K, Q and the statistics, warp 3 V and dO (whose
+    // slots also hold the output boxes).
     if (lane == 0) {
       constexpr uint32_t code = kStatusTimeoutProducer;
       auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int row, int outer) {
@@ -593,6 +605,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
       if (lane == 0) {
         mbar_arrive(ds_full);
         mbar_arrive(&st_empty[par]);
+        if (j + 1 < it.n) mbar_arrive(&do_empty[par]);  // the last slot holds the output boxes first
       }
       if (++t == it.first + it.count) t = it.first;
     }
@@ -607,15 +620,21 @@ __global__ void __launch_bounds__(kBwThreads, 1)
     }
     // Warpgroup 0 stores dV, warpgroup 1 dK.  The next item's first products
     // into them follow this thread's next P and dS arrivals.
-    uint8_t* stage = smem + C::kStage + (warp - 4) * 4096;
     const int row0 = it.k0 + quarter * 32;
+    if (it.n == 0) {
+      if (row0 < s.kv_len)
+        bwd_store_zeros((h ? p.dk : p.dv) + ((long long)it.unit * s.kv_len + row0) * s.head_dim,
+                        min(32, s.kv_len - row0), s.head_dim, lane);
+    } else {
+      uint8_t* stage = C::stage(smem, J - 1) + (warp - 4) * 4096;
 #pragma unroll 1
-    for (int c0 = 0; c0 < s.head_dim && row0 < s.kv_len; c0 += 64)
-      bwd_store_box(h ? &tm_dk : &tm_dv, stage, tmem + lane_base + 256 + 128 * h + c0, c0, row0,
-                    it.unit, h ? p.scale : 1.f, it.n == 0, c0 > 0, lane);
-    if (lane == 0) {
-      bulk_wait_read();  // the box goes back to the loader, or to the next item
-      if (it.n > 0) mbar_arrive(v_empty);
+      for (int c0 = 0; c0 < s.head_dim && row0 < s.kv_len; c0 += 64)
+        bwd_store_box(h ? &tm_dk : &tm_dv, stage, tmem + lane_base + 256 + 128 * h + c0, c0, row0,
+                      it.unit, h ? p.scale : 1.f, c0 > 0, lane);
+      if (lane == 0) {
+        bulk_wait_read();  // the slot goes back to the loader
+        mbar_arrive(&do_empty[(J - 1) & 1]);
+      }
     }
     i = next;
     it = next_it;
@@ -670,7 +689,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], 1);
+      mbar_init(&v_empty[i], 1 + 8);  // dP, the elementwise warps
       mbar_init(&s_full[i], 1);
       mbar_init(&ds_full[i], 8);
     }
@@ -678,7 +697,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
     mbar_init(o_done, 1);
     mbar_init(q_empty, 1);
     mbar_init(do_full, 1);
-    mbar_init(do_empty, 1 + 8);  // the last dP, and the output boxes
+    mbar_init(do_empty, 1);
     mbar_init(drain, 2);
     fence_barrier_init();
   }
@@ -713,8 +732,8 @@ __global__ void __launch_bounds__(kBwThreads, 1)
 
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBwRegsLow));
   if (warp == 0 || warp == 3) {
-    // Two loaders: warp 0 Q and K, warp 3 dO and V (dO waits for the output
-    // boxes).
+    // Two loaders: warp 0 Q and K, warp 3 dO and V (whose slots also hold the
+    // output boxes).
     if (lane == 0) {
       constexpr uint32_t code = kStatusTimeoutProducer;
       auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int row, int outer) {
@@ -879,7 +898,11 @@ __global__ void __launch_bounds__(kBwThreads, 1)
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ds_full[J & 1]);
+      if (lane == 0) {
+        mbar_arrive(&ds_full[J & 1]);
+        // The last slot holds the output boxes first.
+        if (j + 1 < it.kr.t_count) mbar_arrive(&v_empty[J & 1]);
+      }
     }
     if (!ok) break;
     const int next = bwd_item(s, kk);
@@ -891,12 +914,19 @@ __global__ void __launch_bounds__(kBwThreads, 1)
       tc_fence_after();
     }
     // Each warpgroup stores its half of the columns.
-    if (quarter * 32 < it.nr && 64 * h < s.head_dim)
-      bwd_store_box(&tm_dq, smem + C::kStage + (warp - 4) * 4096, tmem + lane_base + 384 + 64 * h,
-                    64 * h, it.r0 + quarter * 32, it.run, p.scale, it.kr.t_count == 0, false, lane);
-    if (lane == 0) {
-      bulk_wait_read();  // the box goes back to the loader, or to the next item
-      if (it.kr.t_count > 0) mbar_arrive(do_empty);
+    const int rows = it.nr - quarter * 32;
+    if (it.kr.t_count == 0) {
+      if (rows > 0 && h == 0)
+        bwd_store_zeros(p.dq + ((long long)it.run * s.run + it.r0 + quarter * 32) * s.head_dim,
+                        min(32, rows), s.head_dim, lane);
+    } else {
+      if (rows > 0 && 64 * h < s.head_dim)
+        bwd_store_box(&tm_dq, C::stage(smem, J - 1) + (warp - 4) * 4096, tmem + lane_base + 384 + 64 * h,
+                      64 * h, it.r0 + quarter * 32, it.run, p.scale, false, lane);
+      if (lane == 0) {
+        bulk_wait_read();  // the slot goes back to the loader
+        mbar_arrive(&v_empty[(J - 1) & 1]);
+      }
     }
     i = next;
     it = next_it;

@@ -25,6 +25,9 @@ CASES = [
     (1, 333, 500, 4, 2, 256, True, 200, 30.0, 2),      # wide heads
     (2, 70, 65, 2, 1, 136, False, None, None, 1),      # just over 128 columns
     (1, 1000, 1000, 2, 1, 64, True, None, None, 1),    # several row and key tiles
+    (2, 600, 2400, 16, 16, 128, True, 300, None, 1),   # more tiles than SMs, most keys hidden
+    (2, 3000, 700, 8, 8, 96, True, None, 30.0, 2),     # more tiles than SMs, most rows empty
+    (3, 290, 1200, 32, 16, 40, True, 64, None, 1),     # the same with one box of columns
 ]
 
 
