@@ -88,6 +88,29 @@ __host__ __device__ __forceinline__ void bwd_row_tiles(const BwdShape& s, int k0
   }
 }
 
+// Whether any row of a row tile fails to see any of the `keys` keys from k0 on:
+// only then are scores masked one by one.
+__device__ __forceinline__ bool bwd_need_mask(const BwdShape& s, const MaskSpec& ms, int r0, int nr,
+                                              int k0, int keys) {
+  if (!(s.causal || s.window > 0)) return k0 + keys > s.kv_len;
+  int i0 = r0, i1 = r0 + nr - 1;
+  if (s.run != s.q_len) {
+    if (nr >= s.q_len) {
+      i0 = 0;
+      i1 = s.q_len - 1;
+    } else {
+      i0 = (int)((unsigned)i0 % (unsigned)s.q_len);
+      i1 = (int)((unsigned)i1 % (unsigned)s.q_len);
+      if (i1 < i0) {
+        i0 = 0;
+        i1 = s.q_len - 1;
+      }
+    }
+  }
+  const int base = s.kv_len - s.q_len;
+  return !(k0 >= first_key(ms, base + i1) && k0 + keys - 1 <= last_key(ms, base + i0));
+}
+
 // delta and lse of every row into the tiled statistics, one block per tile.
 // A tile's rows are one contiguous stretch of dO and of O, read in 16-byte
 // pieces whatever head_dim is; the pieces' dot products meet in shared memory
@@ -176,7 +199,7 @@ struct BwdMmaCfg {
   static constexpr int kPitch = KS * 16 + 8;  // elements: rows 16 bytes off a multiple of 128
   static constexpr int kTileElems = kBmTile * kPitch;
   static constexpr int kPPitch = kBmTile + 8;
-  static constexpr int kSmemBytes = (6 * kTileElems + 2 * kBmTile * kPPitch) * 2 + 4 * kBmTile * 4;
+  static constexpr int kSmemBytes = (6 * kTileElems + 2 * kBmTile * kPPitch) * 2 + 6 * kBmTile * 4;
 };
 
 // n rows x D of a [rows][D] matrix into a padded tile, zeros elsewhere
@@ -203,8 +226,8 @@ __global__ void __launch_bounds__(kBmThreads, 1) bwd_mma_kernel(const BwdParams 
   __nv_bfloat16* str = own2 + C::kTileElems;       // two buffers of Q, dO or K, V
   __nv_bfloat16* pm = str + 4 * C::kTileElems;     // P  [own row][streamed row]
   __nv_bfloat16* dm = pm + kBmTile * C::kPPitch;   // dS
-  float* st2 = (float*)(dm + kBmTile * C::kPPitch);  // two buffers: 64 times -lse, 64 delta of
-                                                     // the query rows
+  // Two buffers for the query rows: 64 times -lse, 64 delta, 64 positions.
+  float* st2 = (float*)(dm + kBmTile * C::kPPitch);
   if (threadIdx.x == 0 && !kDQ) {  // the statistics; then dQ may start (see backward_sm100.cuh)
     grid_wait();
     grid_launch_dependents();
@@ -259,10 +282,11 @@ __global__ void __launch_bounds__(kBmThreads, 1) bwd_mma_kernel(const BwdParams 
     const long long off = (kDQ ? unit * s.kv_len + row0 : run * s.run + row0) * (long long)D;
     bwd_load_tile<KS>(s1, (kDQ ? p.k : p.q) + off, D, n);
     bwd_load_tile<KS>(s1 + C::kTileElems, (kDQ ? p.v : p.dout) + off, D, n);
-    if (threadIdx.x < 128) {
+    if (threadIdx.x < 192) {
       const int w = threadIdx.x >> 6, r = threadIdx.x & 63, q_row0 = kDQ ? own_row0 : row0;
-      st2[(it & 1) * 128 + threadIdx.x] =
-          p.stats[(run * s.tiles + (q_row0 >> 7)) * 256 + w * 128 + (q_row0 & 127) + r];
+      st2[(it & 1) * 192 + threadIdx.x] =
+          w < 2 ? p.stats[(run * s.tiles + (q_row0 >> 7)) * 256 + w * 128 + (q_row0 & 127) + r]
+                : __int_as_float(s.kv_len - s.q_len + (q_row0 + r) % s.q_len);
     }
     cp_async_commit();
   };
@@ -275,10 +299,12 @@ __global__ void __launch_bounds__(kBmThreads, 1) bwd_mma_kernel(const BwdParams 
   }
   for (int it = 0; it < steps; ++it) {
     const int str_row0 = (first + it % count) * kBmTile;
-    const int q_row0 = kDQ ? own_row0 : str_row0;
+    const int q_row0 = kDQ ? own_row0 : str_row0, k_row0 = kDQ ? str_row0 : own_row0;
+    const bool need_mask =
+        bwd_need_mask(s, ms, q_row0, min(kBmTile, s.run - q_row0), k_row0, kBmTile);
     const __nv_bfloat16* str1 = str + (it & 1) * 2 * C::kTileElems;
     const __nv_bfloat16* str2 = str1 + C::kTileElems;
-    const float* st = st2 + (it & 1) * 128;
+    const float* st = st2 + (it & 1) * 192;
     if (it + 1 < steps) {  // its buffer was last read before the loop's closing barrier
       fetch(it + 1);
       cp_async_wait<1>();
@@ -315,34 +341,42 @@ __global__ void __launch_bounds__(kBmThreads, 1) bwd_mma_kernel(const BwdParams 
         }
       }
     }
-    // P and dS, rounded to bf16 for the tensor cores as the forward's P is.
+    // P and dS in place of S and dP; hidden pairs become zeros, whatever they
+    // were.  Element e of piece n: own row m0 + g + 8 (e / 2), streamed row
+    // n0 + 8 n + 2 t4 + e % 2.
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int qr = kDQ ? m0 + g + 8 * (e >> 1) : n0 + n * 8 + 2 * t4 + (e & 1);
+        float t = 0.f, y;
+        if (p.softcap) {
+          t = tanh_accurate(sc[n][e] * p.cap_in);
+          y = p.cap_out * t;
+        } else {
+          y = sc[n][e] * p.logit_scale;
+        }
+        sc[n][e] = ex2(y + st[qr]);
+        dp[n][e] = sc[n][e] * (dp[n][e] - st[64 + qr]) * (1.f - t * t);
+      }
+    if (need_mask) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int own = m0 + g + 8 * (e >> 1), col = n0 + n * 8 + 2 * t4 + (e & 1);
+          const int key = k_row0 + (kDQ ? col : own), qpos = __float_as_int(st[128 + (kDQ ? own : col)]);
+          if (key < first_key(ms, qpos) || key > last_key(ms, qpos)) sc[n][e] = dp[n][e] = 0.f;
+        }
+    }
+    // Rounded to bf16 for the tensor cores as the forward's P is.
 #pragma unroll
     for (int n = 0; n < 4; ++n)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int own = m0 + g + 8 * h, col = n0 + n * 8 + 2 * t4;
-        float pv[2], dv[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int qr = kDQ ? own : col + e, kr = kDQ ? col + e : own;
-          const int key = (kDQ ? str_row0 : own_row0) + kr;
-          const int qpos = s.kv_len - s.q_len + (q_row0 + qr) % s.q_len;
-          const bool see = key >= first_key(ms, qpos) && key <= last_key(ms, qpos);
-          const float x = sc[n][2 * h + e];
-          float t = 0.f, y;
-          if (p.softcap) {
-            t = tanh_accurate(x * p.cap_in);
-            y = p.cap_out * t;
-          } else {
-            y = x * p.logit_scale;
-          }
-          const float pr = see ? ex2(y + st[qr]) : 0.f;
-          const float d = pr * (dp[n][2 * h + e] - st[64 + qr]) * (1.f - t * t);
-          pv[e] = pr;
-          dv[e] = see ? d : 0.f;
-        }
-        if (!kDQ) *(uint32_t*)(pm + own * C::kPPitch + col) = pack_bf16(pv[0], pv[1]);
-        *(uint32_t*)(dm + own * C::kPPitch + col) = pack_bf16(dv[0], dv[1]);
+        const int off = (m0 + g + 8 * h) * C::kPPitch + n0 + n * 8 + 2 * t4;
+        if (!kDQ) *(uint32_t*)(pm + off) = pack_bf16(sc[n][2 * h], sc[n][2 * h + 1]);
+        *(uint32_t*)(dm + off) = pack_bf16(dp[n][2 * h], dp[n][2 * h + 1]);
       }
     __syncthreads();
     // Outputs: 16 own rows x half of the columns, over the 64 streamed rows.

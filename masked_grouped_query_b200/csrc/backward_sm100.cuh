@@ -37,7 +37,7 @@
 // everywhere, so on small problems the two run side by side, and on large ones
 // dQ's CTAs take each SM as it becomes free.  The chain: the dK/dV kernel
 // waits for the statistics, then lets dQ's CTAs start (the statistics are
-// therefore complete for them too); every dQ CTA waits for the dK/dV kernel
+// therefore complete for them too); dQ's last CTA waits for the dK/dV kernel
 // before it ends, so that whatever follows in the stream finds both done.
 // All waits are bounded.
 #pragma once
@@ -74,29 +74,6 @@ struct BwdCfg {
     return DCH == 1 ? smem + kStage : smem + kRing2 + (last_tile & 1) * kTileBytes;
   }
 };
-
-// Whether any row of a row tile fails to see any key of a key tile: only then
-// are scores masked one by one.
-__device__ __forceinline__ bool bwd_need_mask(const BwdShape& s, const MaskSpec& ms, int r0, int nr,
-                                              int k0) {
-  if (!(s.causal || s.window > 0)) return k0 + 127 >= s.kv_len;
-  int i0 = r0, i1 = r0 + nr - 1;
-  if (s.run != s.q_len) {
-    if (nr >= s.q_len) {
-      i0 = 0;
-      i1 = s.q_len - 1;
-    } else {
-      i0 = (int)((unsigned)i0 % (unsigned)s.q_len);
-      i1 = (int)((unsigned)i1 % (unsigned)s.q_len);
-      if (i1 < i0) {
-        i0 = 0;
-        i1 = s.q_len - 1;
-      }
-    }
-  }
-  const int base = s.kv_len - s.q_len;
-  return !(k0 >= first_key(ms, base + i1) && k0 + 127 <= last_key(ms, base + i0));
-}
 
 // P of 32 columns from 32 raw scores (nl: -lse of their rows, in pairs), and
 // with a softcap the factors 1 - tanh^2 that dS takes.  Every 2^x is MUFU's:
@@ -523,7 +500,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
     int t = it.first;
     for (int j = 0; j < it.n; ++j, ++J) {
       const int r0 = t * 128, nr = min(128, s.run - r0);
-      const bool need_mask = bwd_need_mask(s, ms, r0, nr, it.k0);
+      const bool need_mask = bwd_need_mask(s, ms, r0, nr, it.k0, 128);
       const uint32_t par = J & 1, dpar = (J / 2) & 1;
       f2 keep[32];
       const float* st = stats + par * 256 + 64 * h;
@@ -933,7 +910,8 @@ __global__ void __launch_bounds__(kBwThreads, 1)
     }
     if (lane == 0) bulk_wait_all();  // stores done before the CTA exits
   }
-  if (threadIdx.x == 0) grid_wait();
+  // One CTA is enough: the kernel has not ended before it has.
+  if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) grid_wait();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
