@@ -81,3 +81,55 @@ def test_rotary(case, dtypes):
                 check(ko, k, pos, sm, osm, **kw)
             else:
                 assert ko is None
+
+
+def test_in_place_and_back_again():
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.randn(2, 4, 50, 128, generator=g, device="cuda")
+    k = torch.randn(2, 2, 50, 128, generator=g, device="cuda")
+    pos = torch.randint(0, 1 << 20, (3, 2, 50), generator=g, device="cuda")
+    want = mgq.rotary(q, k, pos, sections=(16, 24, 20))
+    a, b = q.clone(), k.clone()
+    r = mgq.rotary(a, b, pos, sections=(16, 24, 20), out=(a, b))
+    assert r[0] is a and r[1] is b
+    assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+    assert torch.equal(a[..., 120:], q[..., 120:])      # the tail stays
+    back = mgq.rotary(a, b, pos, sections=(16, 24, 20), inverse=True)
+    # Two rotations, each off by at most ANGLE and a rounding of the pair's magnitudes.
+    for x, y in zip(back, (q, k)):
+        lim = 4 * (ANGLE + 2.0 ** -24) * (x.abs() + y.abs() + y.abs().max())
+        assert ((x - y).abs() <= lim).all()
+
+
+def test_positions_of_the_smallest_and_largest_calls():
+    # No tokens; and more than 2^31 elements, the last rows against the reference.
+    q = torch.zeros(0, 4, 3, 64, dtype=torch.bfloat16, device="cuda")
+    qo, _ = mgq.rotary(q, None, torch.zeros(1, 0, 3, dtype=torch.int32, device="cuda"), sections=(32,))
+    assert qo.shape == q.shape
+    length, heads = 70400, 240
+    g = torch.Generator(device="cuda").manual_seed(2)
+    q = torch.empty(1, length, heads, 128, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    assert q.numel() > 1 << 31
+    pos = torch.randint(0, 1 << 30, (2, 1, length), generator=g, device="cuda").int()
+    kw = dict(sections=(30, 34), theta=1e6, per_axis=False, interleaved=False, inverse=False)
+    qo, _ = mgq.rotary(q, None, pos, seq_major=True, out_seq_major=False, **kw)
+    check(qo[:, :, -5:].contiguous(), q[:, -5:].contiguous(), pos[:, :, -5:].contiguous(), True, False, **kw)
+
+
+def test_captured_call_and_given_stream():
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q = torch.randn(4, 1, 8, 128, generator=g, device="cuda")
+    k = torch.randn(4, 1, 2, 128, generator=g, device="cuda")
+    pos = torch.randint(0, 1000, (1, 4, 1), generator=g, device="cuda")
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        got = mgq.rotary(q, k, pos, sections=(64,), seq_major=True, out_dtype=torch.bfloat16)
+    for _ in range(3):
+        pos += 1
+        graph.replay()
+        torch.cuda.synchronize()
+        want = mgq.rotary(q, k, pos, sections=(64,), seq_major=True, out_dtype=torch.bfloat16, stream=s)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
