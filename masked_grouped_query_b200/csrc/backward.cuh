@@ -16,6 +16,10 @@
 // of a key tile (four products: S, dP, dV, dK), the other the keys of a row
 // tile (three: S, dP, dQ).  Seven products instead of five, but no atomics,
 // no fp32 dQ buffer and no conversion pass.
+//
+// When there are far fewer tiles than SMs (few keys under many rows, few rows
+// over many keys), the walk of each tile is cut into `splits` parts that leave
+// fp32 partials, which bwd_join_kernel adds in their order.
 #pragma once
 
 #include "mask.cuh"
@@ -49,7 +53,58 @@ struct BwdParams {
   float logit_scale;   // log2(e) / sqrt(D)
   float cap_in;        // 1 / (sqrt(D) * cap)
   float cap_out;       // cap * log2(e)
+  // Parts of a tile's walk; with more than one, their fp32 partials: part i is
+  // [columns rounded up to 16, by 4][tile rows][4].
+  int kv_splits, q_splits;
+  float *part_dk, *part_dv, *part_dq;
 };
+
+// Part sp of splits of n steps: [begin, end).
+__device__ __forceinline__ void bwd_part(int n, int sp, int splits, int& begin, int& end) {
+  begin = 0;
+  end = n;
+  if (splits > 1) {  // 64-bit divisions that the usual walk is spared
+    begin = (int)((long long)n * sp / splits);
+    end = (int)((long long)n * (sp + 1) / splits);
+  }
+}
+
+// Adds the partials of dK, dV (jobs 0, 1) and dQ (job 2) in their order and
+// rounds the sums; a block per tile, rows fastest (coalesced reads).
+struct BwdJoin {
+  struct Job {
+    const float* part;
+    __nv_bfloat16* out;
+    float scale;
+    int splits, rows;  // parts per tile; rows of a run of tiles
+    long long outers, items;
+  } job[3];
+  int tile_rows, head_dim;
+};
+__global__ void __launch_bounds__(256) bwd_join_kernel(const __grid_constant__ BwdJoin j) {
+  const BwdJoin::Job& job = j.job[blockIdx.y];
+  const long long item = blockIdx.x;
+  if (job.splits <= 1 || item >= job.items) return;
+  const int R = j.tile_rows, pad = (j.head_dim + 15) / 16 * 16;
+  const long long outer = item % job.outers;
+  const int row0 = (int)(item / job.outers) * R;
+  const float4* src = reinterpret_cast<const float4*>(job.part) + item * job.splits * (R * pad / 4);
+  for (int e = threadIdx.x; e < R * (j.head_dim / 8); e += 256) {
+    const int row = e % R, c = e / R;
+    if (row0 + row >= job.rows) continue;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+    for (int sp = 0; sp < job.splits; ++sp) {
+      const float4* q = src + (long long)sp * (R * pad / 4) + (2 * c) * R + row;
+      const float4 x = q[0], y = q[R];
+      a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+      b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
+    }
+    const float f = job.scale;
+    *reinterpret_cast<uint4*>(job.out + (outer * job.rows + row0 + row) * j.head_dim + 8 * c) =
+        make_uint4(pack_bf16(a.x * f, a.y * f), pack_bf16(a.z * f, a.w * f),
+                   pack_bf16(b.x * f, b.y * f), pack_bf16(b.z * f, b.w * f));
+  }
+}
 
 __host__ __device__ __forceinline__ MaskSpec bwd_mask(const BwdShape& s) {
   return MaskSpec{s.q_len, s.kv_len, s.causal, s.window};
@@ -240,29 +295,30 @@ __global__ void __launch_bounds__(kBmThreads, 1) bwd_mma_kernel(const BwdParams 
   const int D = s.head_dim;
   const MaskSpec ms = bwd_mask(s);
 
-  // Own tile, and the streamed tiles: `outer` runs of `count` tiles from `first`.
+  // Own tile, and the steps [begin, end) of the walk over the streamed ones:
+  // step i is tile first + i % count of run i / count.
+  const int splits = kDQ ? p.q_splits : p.kv_splits;
+  const int u = (int)(blockIdx.x / (unsigned)splits), sp = (int)(blockIdx.x % (unsigned)splits);
   long long run0, unit;
-  int own_row0, own_n, first, count, outer;
+  int own_row0, own_n, first, count, begin, end;
   if (kDQ) {
-    const int tiles64 = (s.run + kBmTile - 1) / kBmTile;
-    run0 = blockIdx.x / tiles64;
-    own_row0 = (int)(blockIdx.x % tiles64) * kBmTile;
+    run0 = u % (int)s.runs;
+    own_row0 = u / (int)s.runs * kBmTile;
     own_n = min(kBmTile, s.run - own_row0);
     unit = run0 / s.runs_per_unit;
     const KeyRange kr = key_range(ms, own_row0, own_n, kBmTile);
     first = kr.t_first;
     count = kr.t_count;
-    outer = 1;
+    bwd_part(count, sp, splits, begin, end);
     bwd_load_tile<KS>(own1, p.q + (run0 * s.run + own_row0) * D, D, own_n);
     bwd_load_tile<KS>(own2, p.dout + (run0 * s.run + own_row0) * D, D, own_n);
   } else {
-    const int ktiles = (s.kv_len + kBmTile - 1) / kBmTile;
-    unit = blockIdx.x / ktiles;
-    own_row0 = (int)(blockIdx.x % ktiles) * kBmTile;
+    unit = u % (int)s.units;
+    own_row0 = u / (int)s.units * kBmTile;
     own_n = min(kBmTile, s.kv_len - own_row0);
     run0 = unit * s.runs_per_unit;
     bwd_row_tiles(s, own_row0, own_row0 + own_n - 1, kBmTile, first, count);
-    outer = s.runs_per_unit;
+    bwd_part(count * s.runs_per_unit, sp, splits, begin, end);
     bwd_load_tile<KS>(own1, p.k + (unit * s.kv_len + own_row0) * D, D, own_n);
     bwd_load_tile<KS>(own2, p.v + (unit * s.kv_len + own_row0) * D, D, own_n);
   }
@@ -278,34 +334,33 @@ __global__ void __launch_bounds__(kBmThreads, 1) bwd_mma_kernel(const BwdParams 
     const long long run = run0 + (kDQ ? 0 : it / count);
     const int row0 = (first + it % count) * kBmTile;
     const int n = min(kBmTile, (kDQ ? s.kv_len : s.run) - row0);
-    __nv_bfloat16* s1 = str + (it & 1) * 2 * C::kTileElems;
+    __nv_bfloat16* s1 = str + ((it - begin) & 1) * 2 * C::kTileElems;
     const long long off = (kDQ ? unit * s.kv_len + row0 : run * s.run + row0) * (long long)D;
     bwd_load_tile<KS>(s1, (kDQ ? p.k : p.q) + off, D, n);
     bwd_load_tile<KS>(s1 + C::kTileElems, (kDQ ? p.v : p.dout) + off, D, n);
     if (threadIdx.x < 192) {
       const int w = threadIdx.x >> 6, r = threadIdx.x & 63, q_row0 = kDQ ? own_row0 : row0;
-      st2[(it & 1) * 192 + threadIdx.x] =
+      st2[((it - begin) & 1) * 192 + threadIdx.x] =
           w < 2 ? p.stats[(run * s.tiles + (q_row0 >> 7)) * 256 + w * 128 + (q_row0 & 127) + r]
                 : __int_as_float(s.kv_len - s.q_len + (q_row0 + r) % s.q_len);
     }
     cp_async_commit();
   };
-  const int steps = outer * count;
-  if (steps > 0) {
-    fetch(0);
+  if (begin < end) {
+    fetch(begin);
   } else {  // never leave with copies in flight
     cp_async_commit();
     cp_async_wait<0>();
   }
-  for (int it = 0; it < steps; ++it) {
+  for (int it = begin; it < end; ++it) {
     const int str_row0 = (first + it % count) * kBmTile;
     const int q_row0 = kDQ ? own_row0 : str_row0, k_row0 = kDQ ? str_row0 : own_row0;
     const bool need_mask =
         bwd_need_mask(s, ms, q_row0, min(kBmTile, s.run - q_row0), k_row0, kBmTile);
-    const __nv_bfloat16* str1 = str + (it & 1) * 2 * C::kTileElems;
+    const __nv_bfloat16* str1 = str + ((it - begin) & 1) * 2 * C::kTileElems;
     const __nv_bfloat16* str2 = str1 + C::kTileElems;
-    const float* st = st2 + (it & 1) * 192;
-    if (it + 1 < steps) {  // its buffer was last read before the loop's closing barrier
+    const float* st = st2 + ((it - begin) & 1) * 192;
+    if (it + 1 < end) {  // its buffer was last read before the loop's closing barrier
       fetch(it + 1);
       cp_async_wait<1>();
     } else {
@@ -414,13 +469,22 @@ __global__ void __launch_bounds__(kBmThreads, 1) bwd_mma_kernel(const BwdParams 
     for (int h = 0; h < 2; ++h) {
       const int r = m0 + g + 8 * h, c = half * KS * 8 + n * 8 + 2 * t4;
       if (r >= own_n || c >= D) continue;
+      if (splits > 1) {
+        const long long at = blockIdx.x * (long long)(kBmTile * ((D + 15) / 16 * 16)) +
+                             ((c >> 2) * kBmTile + r) * 4 + (c & 3);
+        *(float2*)((kDQ ? p.part_dq : p.part_dk) + at) = make_float2(acc1[n][2 * h], acc1[n][2 * h + 1]);
+        if constexpr (!kDQ)
+          *(float2*)(p.part_dv + at) = make_float2(acc2[n][2 * h], acc2[n][2 * h + 1]);
+        continue;
+      }
       const long long off = (out0 + r) * D + c;
       *(uint32_t*)((kDQ ? p.dq : p.dk) + off) =
           pack_bf16(acc1[n][2 * h] * p.scale, acc1[n][2 * h + 1] * p.scale);
       if constexpr (!kDQ)
         *(uint32_t*)(p.dv + off) = pack_bf16(acc2[n][2 * h], acc2[n][2 * h + 1]);
     }
-  if (kDQ && threadIdx.x == 0) grid_wait();
+  // One CTA is enough: the kernel has not ended before it has.
+  if (kDQ && blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) grid_wait();
 }
 
 }  // namespace gqa

@@ -198,6 +198,22 @@ __device__ __forceinline__ void bwd_store_zeros(__nv_bfloat16* dst, int rows, in
     reinterpret_cast<uint4*>(dst)[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
+// The same rows as a part's fp32 partial: columns [0, cols) of the accumulator
+// at tm (lane = row), or zeros for a part without a step.
+__device__ __forceinline__ void bwd_store_part(float* dst, uint32_t tm, int c0, int c1, int row, bool zero) {
+  for (int c = c0; c < c1; c += 16) {
+    uint32_t v[16];
+    tmem_ld16(tm + c, v);
+    tmem_ld_wait();
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      reinterpret_cast<float4*>(dst)[(c / 4 + g) * 128 + row] =
+          zero ? make_float4(0.f, 0.f, 0.f, 0.f)
+               : make_float4(__uint_as_float(v[4 * g]), __uint_as_float(v[4 * g + 1]),
+                             __uint_as_float(v[4 * g + 2]), __uint_as_float(v[4 * g + 3]));
+  }
+}
+
 // Bits lo..hi of a word (none when hi < lo, or outside 0..31).
 __device__ __forceinline__ uint32_t bwd_bits(int lo, int hi) {
   lo = max(lo, 0);
@@ -332,19 +348,27 @@ __global__ void __launch_bounds__(kBwThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  // Item i: unit i % units, key tile i / units, in ascending order: under a
-  // causal mask the first ones have the most rows.
-  const int units = (int)s.units;
-  const int items = units * ((s.kv_len + 127) / 128);
+  // Item i: part i % splits of unit and key tile u = i / splits: unit u % units,
+  // tile u / units, in ascending order: under a causal mask the first ones
+  // have the most rows.  Step j of an item is row tile t + j, wrapping inside
+  // [first, first + count), from run `run` on.
+  const int units = (int)s.units, splits = p.kv_splits;
+  const int items = units * ((s.kv_len + 127) / 128) * splits;
   struct Item {
-    int unit, k0, first, count, n;
+    int unit, k0, first, count, n, run, t;
   };
   auto item_at = [&](int i) {
+    const int u = splits > 1 ? i / splits : i;
     Item t;
-    t.unit = i % units;
-    t.k0 = i / units * 128;
+    t.unit = u % units;
+    t.k0 = u / units * 128;
     bwd_row_tiles(s, t.k0, min(t.k0 + 127, s.kv_len - 1), 128, t.first, t.count);
-    t.n = t.count * s.runs_per_unit;
+    int begin, end;
+    bwd_part(t.count * s.runs_per_unit, i - u * splits, splits, begin, end);
+    t.n = end - begin;
+    const int skip = begin > 0 ? begin / t.count : 0;
+    t.run = t.unit * s.runs_per_unit + skip;
+    t.t = t.first + begin - skip * t.count;
     return t;
   };
 
@@ -373,7 +397,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
         if (first) load(sk, &tm_k, k_full, it.k0, it.unit);
         else load(sv, &tm_v, v_full, it.k0, it.unit);
         ++n1;
-        int run = it.unit * s.runs_per_unit, t = it.first;
+        int run = it.run, t = it.t;
         for (int j = 0; j < it.n; ++j, ++J) {
           const int q3 = J % 3, d2 = J & 1;
           if (first) {
@@ -497,7 +521,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
     int qlo, qhi;
     bwd_query_range(s, key, key, qlo, qhi);
     if (key >= s.kv_len) qhi = -1;
-    int t = it.first;
+    int t = it.t;
     for (int j = 0; j < it.n; ++j, ++J) {
       const int r0 = t * 128, nr = min(128, s.run - r0);
       const bool need_mask = bwd_need_mask(s, ms, r0, nr, it.k0, 128);
@@ -598,7 +622,12 @@ __global__ void __launch_bounds__(kBwThreads, 1)
     // Warpgroup 0 stores dV, warpgroup 1 dK.  The next item's first products
     // into them follow this thread's next P and dS arrivals.
     const int row0 = it.k0 + quarter * 32;
-    if (it.n == 0) {
+    if (splits > 1) {
+      const int d_pad = (s.head_dim + 15) / 16 * 16;
+      bwd_store_part((h ? p.part_dk : p.part_dv) + (long long)i * 128 * d_pad,
+                     tmem + lane_base + 256 + 128 * h, 0, d_pad, quarter * 32 + lane, it.n == 0);
+      if (lane == 0 && it.n > 0) mbar_arrive(&do_empty[(J - 1) & 1]);
+    } else if (it.n == 0) {
       if (row0 < s.kv_len)
         bwd_store_zeros((h ? p.dk : p.dv) + ((long long)it.unit * s.kv_len + row0) * s.head_dim,
                         min(32, s.kv_len - row0), s.head_dim, lane);
@@ -687,23 +716,29 @@ __global__ void __launch_bounds__(kBwThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  // Item i: run i % runs, row tile from the last down: under a causal mask
-  // the last ones have the most keys.  Runs of one kv head follow each other
-  // and share K and V in L2.
+  // Item i: part i % splits of run and row tile u = i / splits: run u % runs,
+  // tiles from the last down: under a causal mask the last ones have the most
+  // keys.  Runs of one kv head follow each other and share K and V in L2.
   const MaskSpec ms = bwd_mask(s);
-  const int runs = (int)s.runs, items = runs * s.tiles;
+  const int runs = (int)s.runs, splits = p.q_splits, items = runs * s.tiles * splits;
   struct Item {
-    int run, unit, r0, nr, tile;
+    int run, unit, r0, nr, tile, part;
     KeyRange kr;
   };
   auto item_at = [&](int i) {
+    const int u = splits > 1 ? i / splits : i, sp = i - u * splits;
     Item t;
-    t.run = i % runs;
-    t.tile = s.tiles - 1 - i / runs;
+    t.run = u % runs;
+    t.tile = s.tiles - 1 - u / runs;
+    t.part = (t.tile * runs + t.run) * splits + sp;
     t.r0 = t.tile * 128;
     t.nr = min(128, s.run - t.r0);
     t.unit = t.run / s.runs_per_unit;
     t.kr = key_range(ms, t.r0, t.nr, 128);
+    int begin, end;
+    bwd_part(t.kr.t_count, sp, splits, begin, end);
+    t.kr.t_first += begin;
+    t.kr.t_count = end - begin;
     return t;
   };
 
@@ -892,7 +927,12 @@ __global__ void __launch_bounds__(kBwThreads, 1)
     }
     // Each warpgroup stores its half of the columns.
     const int rows = it.nr - quarter * 32;
-    if (it.kr.t_count == 0) {
+    if (splits > 1) {
+      const int d_pad = (s.head_dim + 15) / 16 * 16;
+      bwd_store_part(p.part_dq + (long long)it.part * 128 * d_pad, tmem + lane_base + 384, 64 * h,
+                     min(64 * h + 64, d_pad), r, it.kr.t_count == 0);
+      if (lane == 0 && it.kr.t_count > 0) mbar_arrive(&v_empty[(J - 1) & 1]);
+    } else if (it.kr.t_count == 0) {
       if (rows > 0 && h == 0)
         bwd_store_zeros(p.dq + ((long long)it.run * s.run + it.r0 + quarter * 32) * s.head_dim,
                         min(32, rows), s.head_dim, lane);

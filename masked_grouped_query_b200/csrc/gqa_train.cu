@@ -77,8 +77,57 @@ int bwd_shape(int batch, int q_len, int kv_len, int hq, int hkv, int d, int caus
   return GQA_ATTN_OK;
 }
 
-size_t bwd_scratch_bytes(const BwdShape& s) {
-  return (size_t)s.runs * (size_t)s.tiles * 256 * sizeof(float);
+// How the walks are cut, and where the scratch holds what.
+struct BwdPlan {
+  int tile;  // rows of a key or row tile: 128 (tcgen05) or 64
+  long long key_tiles, row_tiles;
+  int kv_splits, q_splits;
+  size_t off_dk, off_dv, off_dq, bytes;
+};
+
+// Parts of a walk of `steps` steps, `items` walks in all.  A part's start and
+// its share of the join cost about as much as four steps, so no part is
+// shorter, and walks under twelve steps (of the mma.sync kernels: eight, whose
+// step is the longer one) stay whole; the parts fill one CTA per SM of the
+// full GPU at most (a fixed number: the scratch size is host arithmetic).
+// Measured, microseconds whole and cut (batch, queries, keys, heads, width):
+//   3, 3352, 64, 12:4, 32:  248 and 78     1, 1, 32768, 8:1, 128: 295 and 82
+//   1, 2048, 2048, 4:1, 128: 115 and 48    2, 1, 4096, 32:8, 128: 60 and 49
+//   1, 2048, 2048, 1:1, 128: 36 and 27     1, 2048, 2048, 1:1, 256: 161 and 92
+// and with 8 steps (1, 1024, 1024, 8:8, 64) 21 and 26, or in parts of one or
+// two steps 27 to 41 where parts of four take 23 to 27; mma.sync with 10 steps
+// (1, 600, 600, 2:1, 256) 60 and 41.
+constexpr int kBwSplitCtas = 148;
+int bwd_splits(long long items, long long steps, int tile) {
+  if (items <= 0 || steps < (tile == 64 ? 8 : 12) || 2 * items > kBwSplitCtas) return 1;
+  const long long fit = kBwSplitCtas / items, most = steps / 4;
+  return (int)(fit < most ? fit : most);
+}
+
+BwdPlan bwd_plan(const BwdShape& s, bool may_split) {
+  BwdPlan pl;
+  pl.tile = s.head_dim > 128 ? 64 : 128;
+  pl.key_tiles = s.units * ceil_div(s.kv_len, pl.tile);
+  pl.row_tiles = s.runs * ceil_div(s.run, pl.tile);
+  // The longest walk: every tile of the other side, or what a window shows.
+  long long rows = ceil_div(s.run, pl.tile), keys = ceil_div(s.kv_len, pl.tile);
+  if (s.window > 0) {
+    const long long span = s.run == s.q_len ? pl.tile : s.q_len;  // positions in a row tile
+    const long long seen = ((long long)s.window + span + pl.tile - 2) / pl.tile + 1;
+    if (s.run == s.q_len && seen < rows) rows = seen;
+    if (seen < keys) keys = seen;
+  }
+  pl.kv_splits = may_split ? bwd_splits(pl.key_tiles, rows * s.runs_per_unit, pl.tile) : 1;
+  pl.q_splits = may_split ? bwd_splits(pl.row_tiles, keys, pl.tile) : 1;
+  auto align = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  const size_t part = (size_t)pl.tile * ((s.head_dim + 15) / 16 * 16) * sizeof(float);
+  const size_t kv = pl.kv_splits > 1 ? align((size_t)pl.key_tiles * pl.kv_splits * part) : 0;
+  const size_t q = pl.q_splits > 1 ? align((size_t)pl.row_tiles * pl.q_splits * part) : 0;
+  pl.off_dk = (size_t)s.runs * (size_t)s.tiles * 256 * sizeof(float);
+  pl.off_dv = pl.off_dk + kv;
+  pl.off_dq = pl.off_dv + kv;
+  pl.bytes = pl.off_dq + q;
+  return pl;
 }
 
 // A launch that may start before the kernel ahead of it in the stream ends
@@ -108,11 +157,11 @@ int launch_bwd_mma(const BwdParams& p, int device, cudaStream_t st) {
   if (rc == GQA_ATTN_OK) rc = allow_smem(bwd_mma_kernel<KS, true>, C::kSmemBytes, device, done_q);
   if (rc != GQA_ATTN_OK) return rc;
   const long long key_tiles = p.sh.units * ceil_div(p.sh.kv_len, kBmTile);
-  if ((rc = launch_after("launch(backward dK dV)", bwd_mma_kernel<KS, false>, key_tiles, kBmThreads,
+  if ((rc = launch_after("launch(backward dK dV)", bwd_mma_kernel<KS, false>, key_tiles * p.kv_splits, kBmThreads,
                          C::kSmemBytes, st, p)) != GQA_ATTN_OK)
     return rc;
   const long long row_tiles = p.sh.runs * ceil_div(p.sh.run, kBmTile);
-  return launch_after("launch(backward dQ)", bwd_mma_kernel<KS, true>, row_tiles, kBmThreads,
+  return launch_after("launch(backward dQ)", bwd_mma_kernel<KS, true>, row_tiles * p.q_splits, kBmThreads,
                       C::kSmemBytes, st, p);
 }
 
@@ -155,7 +204,8 @@ int launch_bwd_sm100(const BwdParams& p, int device, int sms, cudaStream_t st) {
     if ((rc = gqa_host::tensor_map(m.map, m.base, s.head_dim, m.rows ? s.run : s.kv_len,
                                    m.rows ? s.runs : s.units, m.box)) != GQA_ATTN_OK)
       return rc;
-  const long long key_tiles = s.units * ceil_div(s.kv_len, 128), row_tiles = s.runs * s.tiles;
+  const long long key_tiles = s.units * ceil_div(s.kv_len, 128) * p.kv_splits;
+  const long long row_tiles = s.runs * s.tiles * p.q_splits;
   if ((rc = launch_after("launch(backward dK dV)", bwd_dkdv_kernel<DCH, kCap>,
                          key_tiles < sms ? key_tiles : sms, kBwThreads, C::kSmemBytes, st, q, dout, k,
                          v, dk, dv, p)) != GQA_ATTN_OK)
@@ -210,7 +260,7 @@ int gqa_attn_bwd_scratch(int batch, int q_len, int kv_len, int num_q_heads, int 
   const int rc = bwd_shape(batch, q_len, kv_len, num_q_heads, num_kv_heads, head_dim, causal,
                            window, &s);
   if (rc != GQA_ATTN_OK) return rc;
-  if (bytes) *bytes = bwd_scratch_bytes(s);
+  if (bytes) *bytes = bwd_plan(s, true).bytes;
   return GQA_ATTN_OK;
 }
 
@@ -234,7 +284,10 @@ int gqa_attn_bwd(const void* dout, const void* q, const void* k, const void* v, 
        (uintptr_t)scratch) & 15u)
     return GQA_ATTN_ERR_MISALIGNED;
   const bool work = q_bytes && kv_bytes;
-  const size_t need = work ? bwd_scratch_bytes(s) : 0;
+  // (force_path 1 takes the mma.sync kernels for narrow heads too, uncut.)
+  const bool narrow_mma = head_dim <= 128 && gqa_host::forced_path() == 1;
+  const BwdPlan pl = bwd_plan(s, !narrow_mma);
+  const size_t need = work ? pl.bytes : 0;
   if (need && !scratch) return GQA_ATTN_ERR_NULL_POINTER;
   if (scratch_bytes < need)
     return detail(GQA_ATTN_ERR_ARG, "backward scratch of %zu bytes, needs %zu", scratch_bytes, need);
@@ -267,6 +320,11 @@ int gqa_attn_bwd(const void* dout, const void* q, const void* k, const void* v, 
   p.dk = (__nv_bfloat16*)dk;
   p.dv = (__nv_bfloat16*)dv;
   p.stats = (const float*)scratch;
+  p.kv_splits = pl.kv_splits;
+  p.q_splits = pl.q_splits;
+  p.part_dk = (float*)((char*)scratch + pl.off_dk);
+  p.part_dv = (float*)((char*)scratch + pl.off_dv);
+  p.part_dq = (float*)((char*)scratch + pl.off_dq);
   p.softcap = softcap > 0.f;
   p.scale = 1.0f / std::sqrt((float)head_dim);
   p.logit_scale = kLog2e32 * p.scale;
@@ -276,14 +334,28 @@ int gqa_attn_bwd(const void* dout, const void* q, const void* k, const void* v, 
       p.dout, (const __nv_bfloat16*)o, lse, dlse, (float*)scratch, s);
   if ((rc = launched("launch(backward statistics)")) != GQA_ATTN_OK) return rc;
   // The tcgen05 kernels hold dK and dV of 128 columns each in TMEM next to the
-  // scores: wider heads stay on mma.sync (force_path 1 does for every width).
-  if (head_dim > 128) return launch_bwd_mma<16>(p, device, st);
-  if (gqa_host::forced_path() == 1) return launch_bwd_mma<8>(p, device, st);
-  if (head_dim <= 64)
-    return p.softcap ? launch_bwd_sm100<1, true>(p, device, sms, st)
-                     : launch_bwd_sm100<1, false>(p, device, sms, st);
-  return p.softcap ? launch_bwd_sm100<2, true>(p, device, sms, st)
+  // scores: wider heads stay on mma.sync.
+  if (head_dim > 128)
+    rc = launch_bwd_mma<16>(p, device, st);
+  else if (narrow_mma)
+    rc = launch_bwd_mma<8>(p, device, st);
+  else if (head_dim <= 64)
+    rc = p.softcap ? launch_bwd_sm100<1, true>(p, device, sms, st)
+                   : launch_bwd_sm100<1, false>(p, device, sms, st);
+  else
+    rc = p.softcap ? launch_bwd_sm100<2, true>(p, device, sms, st)
                    : launch_bwd_sm100<2, false>(p, device, sms, st);
+  if (rc != GQA_ATTN_OK || (pl.kv_splits == 1 && pl.q_splits == 1)) return rc;
+  BwdJoin j;
+  j.job[0] = {p.part_dk, p.dk, p.scale, pl.kv_splits, kv_len, s.units, pl.key_tiles};
+  j.job[1] = {p.part_dv, p.dv, 1.0f, pl.kv_splits, kv_len, s.units, pl.key_tiles};
+  j.job[2] = {p.part_dq, p.dq, p.scale, pl.q_splits, s.run, s.runs, pl.row_tiles};
+  j.tile_rows = pl.tile;
+  j.head_dim = head_dim;
+  const long long most = (pl.kv_splits > 1 ? pl.key_tiles : 0) > (pl.q_splits > 1 ? pl.row_tiles : 0)
+                             ? pl.key_tiles : pl.row_tiles;
+  bwd_join_kernel<<<dim3((unsigned)most, 3), 256, 0, st>>>(j);
+  return launched("launch(backward join)");
 }
 
 int gqa_attn_rotary(const void* q, const void* k, void* q_out, void* k_out, const void* positions,

@@ -28,6 +28,14 @@ CASES = [
     (2, 600, 2400, 16, 16, 128, True, 300, None, 1),   # more tiles than SMs, most keys hidden
     (2, 3000, 700, 8, 8, 96, True, None, 30.0, 2),     # more tiles than SMs, most rows empty
     (3, 290, 1200, 32, 16, 40, True, 64, None, 1),     # the same with one box of columns
+    # Few tiles, long walks: cut into parts that are joined.
+    (1, 3000, 64, 3, 1, 32, False, None, None, 4),     # few keys under many rows
+    (2, 1500, 200, 2, 1, 128, True, None, 30.0, 2),    # the same, most rows empty
+    (1, 2, 5000, 8, 2, 128, True, None, None, 1),      # few rows over many keys
+    (1, 3, 7000, 4, 1, 72, True, 3000, 50.0, 4),       # the same, parts without a visible key
+    (1, 1100, 1300, 1, 1, 104, True, None, None, 1),   # both, of uneven length
+    (1, 1400, 90, 2, 1, 200, True, None, None, 1),     # wide heads
+    (1, 5, 2100, 2, 1, 256, False, 1500, 20.0, 1),
 ]
 
 

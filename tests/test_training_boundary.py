@@ -65,8 +65,8 @@ def test_backward_index_limits(lib):
 
 
 def test_scratch_bytes(lib):
-    # 1 KiB for every tile of 128 rows; runs are heads where a mask separates
-    # long ones, whole groups otherwise.
+    # 1 KiB for every tile of 128 rows (runs are heads where a mask separates
+    # long ones, whole groups otherwise) while no walk is cut.
     def tiles(*dims):
         size = ctypes.c_size_t(0)
         assert lib.gqa_attn_bwd_scratch(*dims, ctypes.byref(size)) == 0
@@ -74,7 +74,11 @@ def test_scratch_bytes(lib):
         return size.value // 1024
 
     assert tiles(1, 128, 128, 4, 1, 128, 1, 0) == 4          # 512 rows of one group
-    assert tiles(2, 1, 4096, 32, 8, 128, 1, 0) == 16         # 4 rows each
+    assert tiles(32, 1, 4096, 32, 8, 128, 1, 0) == 256       # 4 rows each
+    # 16 row tiles over 32 key tiles: 8 parts each, of 128 x 128 floats.
+    assert tiles(2, 1, 4096, 32, 8, 128, 1, 0) == 16 + 16 * 8 * 64
+    # One key tile under 40 row tiles: 10 parts of dK and of dV, 128 x 64 floats.
+    assert tiles(1, 5120, 100, 1, 1, 64, 0, 0) == 40 + 2 * 10 * 32
     assert tiles(1, 300, 300, 4, 2, 64, 1, 0) == 4 * 3       # heads apart
     assert tiles(1, 300, 300, 4, 2, 64, 0, 0) == 2 * 5       # 600 rows of two heads
     assert tiles(1, 300, 300, 4, 2, 64, 0, 7) == 4 * 3
