@@ -46,64 +46,84 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, *, 
     output layout and type as the input's.  ``out`` is a (q_out, k_out) pair of
     tensors to write, q and k themselves where type and layout do not change.
     """
-    tensors = [("q", q)] + ([] if k is None else [("k", k)])
-    for n, t in tensors:
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{n} must be a torch.Tensor")
-        if t.dtype not in _DTYPES or t.dtype != q.dtype:
-            raise TypeError(f"q and k must both be bfloat16 or float32, got {n} {t.dtype}")
-        if t.dim() != 4 or not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{n} must be a contiguous 4-D CUDA tensor")
-        if t.device != q.device:
-            raise ValueError(f"{n} is on {t.device}, q on {q.device}")
-    hd, ld = (2, 1) if seq_major else (1, 2)
-    b, length, hq, d = q.shape[0], q.shape[ld], q.shape[hd], q.shape[3]
-    hkv = 0 if k is None else k.shape[hd]
-    if k is not None and (k.shape[0], k.shape[ld], k.shape[3]) != (b, length, d):
-        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}")
+    _check("q", q, q)
+    if seq_major:
+        b, length, hq, d = q.shape
+    else:
+        b, hq, length, d = q.shape
+    hkv = 0
+    if k is not None:
+        _check("k", k, q)
+        if seq_major:
+            bk, lk, hkv, dk = k.shape
+        else:
+            bk, hkv, lk, dk = k.shape
+        if bk != b or lk != length or dk != d:
+            raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}")
     sections = [int(s) for s in sections]
     if not isinstance(positions, torch.Tensor):
         raise TypeError("positions must be a torch.Tensor")
     if positions.dtype not in (torch.int32, torch.int64):
         raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
-    if tuple(positions.shape) != (len(sections), b, length) or positions.device != q.device \
+    device = q.device
+    if positions.shape != (len(sections), b, length) or positions.device != device \
             or not positions.is_contiguous():
         raise ValueError(f"positions must be contiguous with shape {(len(sections), b, length)} on "
-                         f"{q.device}, got {tuple(positions.shape)} on {positions.device}")
+                         f"{device}, got {tuple(positions.shape)} on {positions.device}")
     if out_seq_major is None:
         out_seq_major = seq_major
     if out_dtype is None:
         out_dtype = q.dtype
-    if out_dtype not in _DTYPES:
+    elif out_dtype not in _DTYPES:
         raise TypeError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
-    if out is not None and (not isinstance(out, (tuple, list)) or len(out) != 2):
+    if out is None:
+        out = (None, None)
+    elif not isinstance(out, (tuple, list)) or len(out) != 2:
         raise TypeError("out must be a pair (q_out, k_out)")
-    outs = []
-    for i, (t, heads) in enumerate(((q, hq), (k, hkv))):
-        o = None if out is None else out[i]
-        if t is None:
-            if o is not None:
-                raise ValueError("out has a k_out, but there is no k")
+    with _on(stream):
+        q_out = _output(out[0], q, (b, length, hq, d) if out_seq_major else (b, hq, length, d),
+                        out_dtype)
+        if k is not None:
+            k_out = _output(out[1], k, (b, length, hkv, d) if out_seq_major
+                            else (b, hkv, length, d), out_dtype)
+        elif out[1] is not None:
+            raise ValueError("out has a k_out, but there is no k")
         else:
-            shape = (b, length, heads, d) if out_seq_major else (b, heads, length, d)
-            if o is None:
-                with _on(stream):
-                    o = torch.empty(shape, dtype=out_dtype, device=q.device)
-            elif (not isinstance(o, torch.Tensor) or tuple(o.shape) != shape
-                  or o.dtype != out_dtype or o.device != q.device or not o.is_contiguous()):
-                raise ValueError(f"out must hold contiguous {out_dtype} tensors of shape {shape} on "
-                                 f"{q.device}")
-        outs.append(o)
+            k_out = None
     flags = ((IN_SEQ_MAJOR if seq_major else 0) | (OUT_SEQ_MAJOR if out_seq_major else 0)
              | (IN_F32 if q.dtype == torch.float32 else 0)
              | (OUT_F32 if out_dtype == torch.float32 else 0)
              | (POS_I64 if positions.dtype == torch.int64 else 0)
              | (INTERLEAVED if interleaved else 0) | (PER_AXIS if per_axis else 0)
              | (INVERSE if inverse else 0))
-    ptr = [None if t is None else t.data_ptr() for t in (q, k, *outs)]
-    with _device(q.device):
-        rc = _lib.load().gqa_attn_rotary(*ptr, positions.data_ptr(), b, length, hq, hkv, d,
-                                         len(sections), (ctypes.c_int * len(sections))(*sections),
-                                         float(theta), flags, _stream_of(stream, q.device))
+    with _device(device):
+        rc = _lib.load().gqa_attn_rotary(
+            q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
+            None if k is None else k_out.data_ptr(), positions.data_ptr(), b, length, hq, hkv, d,
+            len(sections), (ctypes.c_int * len(sections))(*sections), float(theta), flags,
+            _stream_of(stream, device))
     _lib.check(rc, "gqa_attn_rotary")
-    return tuple(outs)
+    return q_out, k_out
+
+
+def _check(name, t, q):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _DTYPES or t.dtype != q.dtype:
+        raise TypeError(f"q and k must both be bfloat16 or float32, got {name} {t.dtype}")
+    if t.dim() != 4 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 4-D CUDA tensor")
+    if t.device != q.device:
+        raise ValueError(f"{name} is on {t.device}, q on {q.device}")
+
+
+def _output(out, like, shape, dtype):
+    if out is None:
+        if dtype == like.dtype and like.shape == shape:
+            return torch.empty_like(like)
+        return like.new_empty(shape, dtype=dtype)
+    if (not isinstance(out, torch.Tensor) or out.shape != shape or out.dtype != dtype
+            or out.device != like.device or not out.is_contiguous()):
+        raise ValueError(f"out must hold contiguous {dtype} tensors of shape {shape} on "
+                         f"{like.device}")
+    return out
