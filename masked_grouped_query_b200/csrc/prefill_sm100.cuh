@@ -725,6 +725,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             const f2 q0 = f2_pack(cc * kTanh5C1, cc * kTanh5C1);
             const f2 q1 = f2_pack(cc * ci2 * kTanh5C3, cc * ci2 * kTanh5C3);
             const f2 q2 = f2_pack(cc * ci2 * ci2 * kTanh5C5, cc * ci2 * ci2 * kTanh5C5);
+            const LogitPoly13 logit13(p.cap_in, p.cap_out);  // kLse only
             f2 acc[4] = {0ull, 0ull, 0ull, 0ull};
             auto group = [&](uint32_t(&sv)[32], int g) {
               float am = fmaxf(fabsf(__uint_as_float(sv[0])), fabsf(__uint_as_float(sv[1])));
@@ -739,20 +740,25 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               }
               uint32_t pk[16];
               if (kLse && poly) {
-                const LogitPoly13 logit(p.cap_in, p.cap_out);
+                f2 pv[16];
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                  pv[c] = exp2_mufu_x2(logit13(
+                      f2_pack(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1])), nb));
+                if (need_mask) {  // a hidden key went through the polynomial as -inf
+#pragma unroll
+                  for (int c = 0; c < 16; ++c) {
+                    float pa, pb;
+                    f2_unpack(pv[c], pa, pb);
+                    const int col = 32 * g + 2 * c;
+                    pv[c] = f2_pack((unsigned)(col - vlo) > vspan ? 0.f : pa,
+                                    (unsigned)(col + 1 - vlo) > vspan ? 0.f : pb);
+                  }
+                }
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
-                  f2 pv = exp2_mufu_x2(
-                      logit(f2_pack(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1])), nb));
-                  if (need_mask) {  // (a hidden key went through the polynomial as -inf)
-                    float pa, pb;
-                    f2_unpack(pv, pa, pb);
-                    const int col = 32 * g + 2 * c;
-                    pv = f2_pack((unsigned)(col - vlo) > vspan ? 0.f : pa,
-                                 (unsigned)(col + 1 - vlo) > vspan ? 0.f : pb);
-                  }
-                  acc[c & 3] = f2_add(acc[c & 3], pv);
-                  pk[c] = pack_bf16_f2(pv);
+                  acc[c & 3] = f2_add(acc[c & 3], pv[c]);
+                  pk[c] = pack_bf16_f2(pv[c]);
                 }
               } else if (poly) {
 #pragma unroll
