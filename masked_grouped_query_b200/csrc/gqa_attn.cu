@@ -151,6 +151,7 @@ struct Plan {
   long long ctas = 0;
   int dch = 2, d_pad = 128;           // prefill: TMA boxes per tile, padded head_dim
   int tiles_per_unit = 0, pairs_per_unit = 0, pair_heads = 0, split_pairs = 0;
+  int head_tiles = 0;       // prefill with lse: row tiles per q head, when none crosses heads
   size_t ws_bytes = 0;      // split partials (o_s, lse_s)
   size_t off_lse = 0;
   size_t ticket_bytes = 0;  // split tickets (kept zero between calls)
@@ -234,14 +235,23 @@ int plan_prefill(const Problem& pr, const DeviceInfo& dev, Plan* pl) {
   pl->d_pad = (pr.d + 15) / 16 * 16;
   pl->tiles_per_unit = (int)ceil_div(pr.rows, kPfM);
   pl->pair_heads = (pr.q_len % kPfM == 0 && pr.group % 2 == 0) ? 1 : 0;
-  pl->pairs_per_unit = pl->pair_heads ? (pr.group / 2) * (pr.q_len / kPfM)
+  int tiles_per_head = pr.q_len / kPfM;
+  if (pr.lse && (pr.causal || pr.window > 0) && pr.q_len >= 256 && pr.q_len % kPfM != 0) {
+    tiles_per_head = (int)ceil_div(pr.q_len, kPfM);
+    pl->head_tiles = tiles_per_head;
+    pl->tiles_per_unit = pr.group * tiles_per_head;
+    pl->pair_heads = pr.group % 2 == 0 ? 1 : 0;
+  }
+  pl->pairs_per_unit = pl->pair_heads ? (pr.group / 2) * tiles_per_head
                                       : (int)ceil_div(pl->tiles_per_unit, 2);
   pl->ctas = pr.units * pl->pairs_per_unit;
   const MaskSpec ms{pr.q_len, pr.kv_len, pr.causal, pr.window};
   int max_tiles = 0;
   for (int t = 0; t < pl->tiles_per_unit; ++t) {
-    const long long r0 = (long long)t * kPfM;
-    const int nr = (int)((pr.rows - r0) < kPfM ? (pr.rows - r0) : kPfM);
+    // With head_tiles: positions within a head (every head has the same).
+    const long long r0 = (long long)(pl->head_tiles ? t % pl->head_tiles : t) * kPfM;
+    const long long left = (pl->head_tiles ? pr.q_len : pr.rows) - r0;
+    const int nr = (int)(left < kPfM ? left : kPfM);
     const KeyRange kr = key_range(ms, r0, nr, kPfN);
     if (kr.t_count > max_tiles) max_tiles = kr.t_count;
   }
@@ -638,8 +648,10 @@ int launch_prefill_k(const Problem& pr, const Plan& pl, DeviceInfo& dev, int csi
   int rc = prefill_setup<DCH, kCapDeg, kSplit, kLse>(dev);
   if (rc != GQA_ATTN_OK) return rc;
   CUtensorMap tq, tk, tv, to;
-  if (encode_map(&tq, q, pr.d, pr.rows, pr.units, kPfM) != GQA_ATTN_OK ||
-      encode_map(&to, o, pr.d, pr.rows, pr.units, 32) != GQA_ATTN_OK ||
+  const long long map_rows = pl.head_tiles ? pr.q_len : pr.rows;
+  const long long map_outer = pl.head_tiles ? pr.units * pr.group : pr.units;
+  if (encode_map(&tq, q, pr.d, map_rows, map_outer, kPfM) != GQA_ATTN_OK ||
+      encode_map(&to, o, pr.d, map_rows, map_outer, 32) != GQA_ATTN_OK ||
       encode_kv_map(&tk, k, pr, kPfN) != GQA_ATTN_OK ||
       encode_kv_map(&tv, v, pr, kPfN) != GQA_ATTN_OK)
     return GQA_ATTN_ERR_LAUNCH;
@@ -660,6 +672,7 @@ int launch_prefill_k(const Problem& pr, const Plan& pl, DeviceInfo& dev, int csi
   p.ws_ml = ws ? (float*)((char*)ws + pl.off_lse) : nullptr;
   p.tickets = (unsigned int*)tickets;
   p.lse = pr.lse;
+  p.head_tiles = pl.head_tiles;
   p.pair_heads = pl.pair_heads;
   p.heavy_first = (pr.causal || pr.window > 0) && !pl.split_pairs ? 1 : 0;
   p.cluster_merge = kSplit == 2 ? csize : 0;
@@ -1097,7 +1110,7 @@ int gqa_attn_selftest_bounded_wait(int limit_us, void* stream) {
   return cudaGetLastError() == cudaSuccess ? GQA_ATTN_OK : GQA_ATTN_ERR_LAUNCH;
 }
 
-int gqa_attn_version(void) { return 300; }
+int gqa_attn_version(void) { return 400; }
 
 // Argument checks of a KV-cache append (nothing launched).  *n_out gets the
 // number of new elements per tensor; GQA_ATTN_OK with *n_out == 0 means

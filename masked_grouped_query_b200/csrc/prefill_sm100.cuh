@@ -114,6 +114,12 @@ struct PrefillParams {
   float* ws_ml;
   unsigned int* tickets;
   float* lse;  // kLse kernels: log-sum-exp per row, natural logarithm ([unit][row])
+  // kLse kernels: row tiles per q head when tiles do not cross heads (the last
+  // one of a head is then partial), or 0.  With a mask, a tile that straddles
+  // two heads visits every key of both: 2047 windowed rows a head took 175 us
+  // in straddling tiles, 2048 took 100.  The Q and O maps are then
+  // (col, query, q head) instead of (col, row, unit).
+  int head_tiles;
 };
 
 // Natural-log log-sum-exp of a row from its base and sum in log2 units
@@ -164,15 +170,18 @@ struct PrefillCfg {
 struct TileInfo {
   int row0;       // first row of the tile in the unit's row block
   int nrows;      // valid rows (0 = no tile)
+  int map_row;    // its coordinates in the Q and O maps
+  int map_outer;
   KeyRange kr;    // key tiles this tile touches
 };
 
+template <bool kLse>
 __device__ __forceinline__ TileInfo prefill_tile(const PrefillParams& p, const MaskSpec& ms,
-                                                 int pair, int which) {
+                                                 int unit, int pair, int which) {
   TileInfo ti;
   int tile;
   if (p.pair_heads) {
-    const int tiles_per_head = p.q_len / kPfM;
+    const int tiles_per_head = kLse && p.head_tiles ? p.head_tiles : p.q_len / kPfM;
     const int pos = pair % tiles_per_head, hp = pair / tiles_per_head;
     tile = (2 * hp + which) * tiles_per_head + pos;
   } else {
@@ -180,6 +189,15 @@ __device__ __forceinline__ TileInfo prefill_tile(const PrefillParams& p, const M
   }
   ti.row0 = tile * kPfM;
   ti.nrows = tile < p.tiles_per_unit ? min(kPfM, p.rows - ti.row0) : 0;
+  ti.map_row = ti.row0;
+  ti.map_outer = unit;
+  if (kLse && p.head_tiles) {
+    const int head = tile / p.head_tiles, pos = tile - head * p.head_tiles;
+    ti.map_row = pos * kPfM;
+    ti.map_outer = unit * (p.rows / p.q_len) + head;
+    ti.row0 = head * p.q_len + ti.map_row;
+    ti.nrows = tile < p.tiles_per_unit ? min(kPfM, p.q_len - ti.map_row) : 0;
+  }
   if (ti.nrows > 0) {
     ti.kr = key_range(ms, ti.row0, ti.nrows, kPfN);
   } else {
@@ -208,7 +226,7 @@ struct PfItem {
   bool busy;
 };
 
-template <int kSplit>
+template <int kSplit, bool kLse>
 __device__ __forceinline__ PfItem prefill_item(const PrefillParams& p, const MaskSpec& ms,
                                                int item) {
   PfItem it;
@@ -223,6 +241,8 @@ __device__ __forceinline__ PfItem prefill_item(const PrefillParams& p, const Mas
     ti.row0 = tile * kPfM;
     ti.nrows = min(kPfM, p.rows - ti.row0);
     ti.kr = key_range(ms, ti.row0, ti.nrows, kPfN);
+    ti.map_row = ti.row0;
+    ti.map_outer = it.unit;
     it.tile[0] = ti;
     it.tile[1] = ti;
     // Split s takes key tiles [ceil(s T / S), ceil((s + 1) T / S)): sizes
@@ -257,7 +277,7 @@ __device__ __forceinline__ PfItem prefill_item(const PrefillParams& p, const Mas
     const int rank = it.pair_index / units;
     it.unit = it.pair_index % units;
     if (p.pair_heads) {
-      const int tiles_per_head = p.q_len / kPfM;
+      const int tiles_per_head = kLse && p.head_tiles ? p.head_tiles : p.q_len / kPfM;
       const int n_hp = p.pairs_per_unit / tiles_per_head;
       pair = (rank % n_hp) * tiles_per_head + (tiles_per_head - 1 - rank / n_hp);
     } else {
@@ -267,8 +287,8 @@ __device__ __forceinline__ PfItem prefill_item(const PrefillParams& p, const Mas
     it.unit = it.pair_index / p.pairs_per_unit;
     pair = it.pair_index % p.pairs_per_unit;
   }
-  it.tile[0] = prefill_tile(p, ms, pair, 0);
-  it.tile[1] = prefill_tile(p, ms, pair, 1);
+  it.tile[0] = prefill_tile<kLse>(p, ms, it.unit, pair, 0);
+  it.tile[1] = prefill_tile<kLse>(p, ms, it.unit, pair, 1);
   const KeyRange& a = it.tile[0].kr;
   const KeyRange& b = it.tile[1].kr;
   if (a.t_count == 0 && b.t_count == 0) {
@@ -417,7 +437,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       bool ok = true;
       for (int kk = 0, item = snake_item(p, 0); item < p.n_items && ok;
            ++kk, item = snake_item(p, kk)) {
-        const PfItem it = prefill_item<kSplit>(p, ms, item);
+        const PfItem it = prefill_item<kSplit, kLse>(p, ms, item);
         if (!it.busy) continue;
         const int kvh = it.unit % p.kv_heads, bidx = it.unit / p.kv_heads;
         if (!v_stream) {
@@ -432,7 +452,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             if (it.tile[t].nrows > 0)
               for (int c = 0; c < DCH; ++c)
                 tma_load_3d(sq + t * C::kTileBytes + c * C::kBoxBytes, &tm_q, q_full, c * 64,
-                            it.tile[t].row0, it.unit);
+                            it.tile[t].map_row, it.tile[t].map_outer);
           ++nq;
         }
         if (it.paired) {
@@ -502,7 +522,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       bool ok = true;
       for (int kk = 0, item = snake_item(p, 0); item < p.n_items && ok;
            ++kk, item = snake_item(p, kk)) {
-        const PfItem it = prefill_item<kSplit>(p, ms, item);
+        const PfItem it = prefill_item<kSplit, kLse>(p, ms, item);
         if (!it.busy) continue;
         if (!(ok = mbar_wait(q_full, nq & 1, kStatusTimeoutMma))) break;
         ++nq;
@@ -682,7 +702,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     bool ok = true;
     for (int kk = 0, item = snake_item(p, 0); item < p.n_items && ok;
          ++kk, item = snake_item(p, kk)) {
-      const PfItem it = prefill_item<kSplit>(p, ms, item);
+      const PfItem it = prefill_item<kSplit, kLse>(p, ms, item);
       const TileInfo ti = t ? it.tile[1] : it.tile[0];
       int lo = 0, hi = -1;  // visible keys of this row (hi < lo: none)
       if (r < ti.nrows) {
@@ -1031,7 +1051,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          tma_store_3d(&tm_o, stage, c0, tile.row0 + quarter * 32, it.unit);
+          tma_store_3d(&tm_o, stage, c0, tile.map_row + quarter * 32, tile.map_outer);
           bulk_commit();
         }
       };

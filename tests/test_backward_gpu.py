@@ -28,6 +28,8 @@ CASES = [
     (2, 600, 2400, 16, 16, 128, True, 300, None, 1),   # more tiles than SMs, most keys hidden
     (2, 3000, 700, 8, 8, 96, True, None, 30.0, 2),     # more tiles than SMs, most rows empty
     (3, 290, 1200, 32, 16, 40, True, 64, None, 1),     # the same with one box of columns
+    (1, 417, 417, 6, 2, 64, True, 100, 20.0, 3),       # ragged heads, an odd group
+    (2, 1153, 1400, 16, 4, 128, True, None, None, 1),  # ragged heads, more tile pairs than SMs
     # Few tiles, long walks: cut into parts that are joined.
     (1, 3000, 64, 3, 1, 32, False, None, None, 4),     # few keys under many rows
     (2, 1500, 200, 2, 1, 128, True, None, 30.0, 2),    # the same, most rows empty
