@@ -144,7 +144,8 @@ int gqa_attn_fwd_lse(const void* q, const void* k, const void* v, void* o, float
  * gradient dlse of lse.  dout, q, o and dq are bf16 of q's shape, k, v, dk
  * and dv bf16 of k's shape, lse and dlse fp32 [batch][num_q_heads][q_len]:
  * dense device memory, 16-byte aligned.  P and ds are rounded to bf16 for the
- * tensor cores, sums are fp32, each gradient is rounded once.  A row without
+ * tensor cores (small problems take two bf16 terms of each), sums are fp32,
+ * each gradient is rounded once.  A row without
  * a visible key (lse = -inf) gives and gets no gradient; a key that no query
  * sees gets zeros.  Masked scores count as exact zeros, but a NaN or an
  * infinity in k, v, q or dout still reaches every gradient whose products

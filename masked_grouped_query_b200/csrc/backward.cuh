@@ -271,7 +271,18 @@ __device__ __forceinline__ void bwd_load_tile(__nv_bfloat16* dst, const __nv_bfl
   }
 }
 
-template <int KS, bool kDQ>
+// Two values as a bf16 pair; with kFine they keep what the rounding left.
+template <bool kFine>
+__device__ __forceinline__ uint32_t bwd_take_bf16(float& a, float& b) {
+  const uint32_t w = pack_bf16(a, b);
+  if constexpr (kFine) {
+    a -= __uint_as_float(w << 16);
+    b -= __uint_as_float(w & 0xffff0000u);
+  }
+  return w;
+}
+
+template <int KS, bool kDQ, bool kFine>
 __global__ void __launch_bounds__(kBmThreads, 1) bwd_mma_kernel(const BwdParams p) {
   using C = BwdMmaCfg<KS>;
   const BwdShape& s = p.sh;
@@ -424,40 +435,48 @@ __global__ void __launch_bounds__(kBmThreads, 1) bwd_mma_kernel(const BwdParams 
           if (key < first_key(ms, qpos) || key > last_key(ms, qpos)) sc[n][e] = dp[n][e] = 0.f;
         }
     }
-    // Rounded to bf16 for the tensor cores as the forward's P is.
+    // Rounded to bf16 for the tensor cores as the forward's P is; when fine, a
+    // second round with what the first rounding left.
+    auto products = [&]() {
 #pragma unroll
-    for (int n = 0; n < 4; ++n)
+      for (int n = 0; n < 4; ++n)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int off = (m0 + g + 8 * h) * C::kPPitch + n0 + n * 8 + 2 * t4;
-        if (!kDQ) *(uint32_t*)(pm + off) = pack_bf16(sc[n][2 * h], sc[n][2 * h + 1]);
-        *(uint32_t*)(dm + off) = pack_bf16(dp[n][2 * h], dp[n][2 * h + 1]);
-      }
-    __syncthreads();
-    // Outputs: 16 own rows x half of the columns, over the 64 streamed rows.
-    {
-      const uint32_t aoff = ((m0 + (lane & 15)) * C::kPPitch + (lane >> 4) * 8) * 2;
-      const uint32_t ad = smem_u32(dm) + aoff, ap = smem_u32(pm) + aoff;
-      const uint32_t boff = (((mi & 1) * 8 + rr) * C::kPitch + half * KS * 8 + (mi >> 1) * 8) * 2;
-      const uint32_t b1 = smem_u32(str1) + boff, b2 = smem_u32(str2) + boff;
+        for (int h = 0; h < 2; ++h) {
+          const int off = (m0 + g + 8 * h) * C::kPPitch + n0 + n * 8 + 2 * t4;
+          if (!kDQ) *(uint32_t*)(pm + off) = bwd_take_bf16<kFine>(sc[n][2 * h], sc[n][2 * h + 1]);
+          *(uint32_t*)(dm + off) = bwd_take_bf16<kFine>(dp[n][2 * h], dp[n][2 * h + 1]);
+        }
+      __syncthreads();
+      // Outputs: 16 own rows x half of the columns, over the 64 streamed rows.
+      {
+        const uint32_t aoff = ((m0 + (lane & 15)) * C::kPPitch + (lane >> 4) * 8) * 2;
+        const uint32_t ad = smem_u32(dm) + aoff, ap = smem_u32(pm) + aoff;
+        const uint32_t boff = (((mi & 1) * 8 + rr) * C::kPitch + half * KS * 8 + (mi >> 1) * 8) * 2;
+        const uint32_t b1 = smem_u32(str1) + boff, b2 = smem_u32(str2) + boff;
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        uint32_t x0, x1, x2, x3, y0 = 0, y1 = 0, y2 = 0, y3 = 0;
-        ldsm_x4(ad + ks * 32, x0, x1, x2, x3);
-        if (!kDQ) ldsm_x4(ap + ks * 32, y0, y1, y2, y3);
+        for (int ks = 0; ks < 4; ++ks) {
+          uint32_t x0, x1, x2, x3, y0 = 0, y1 = 0, y2 = 0, y3 = 0;
+          ldsm_x4(ad + ks * 32, x0, x1, x2, x3);
+          if (!kDQ) ldsm_x4(ap + ks * 32, y0, y1, y2, y3);
 #pragma unroll
-        for (int n = 0; n < KS; n += 2) {
-          uint32_t c0, c1, c2, c3;
-          ldsm_x4_t(b1 + (ks * 16 * C::kPitch + n * 8) * 2, c0, c1, c2, c3);
-          mma_16816(acc1[n], x0, x1, x2, x3, c0, c1);
-          mma_16816(acc1[n + 1], x0, x1, x2, x3, c2, c3);
-          if constexpr (!kDQ) {
-            ldsm_x4_t(b2 + (ks * 16 * C::kPitch + n * 8) * 2, c0, c1, c2, c3);
-            mma_16816(acc2[n], y0, y1, y2, y3, c0, c1);
-            mma_16816(acc2[n + 1], y0, y1, y2, y3, c2, c3);
+          for (int n = 0; n < KS; n += 2) {
+            uint32_t c0, c1, c2, c3;
+            ldsm_x4_t(b1 + (ks * 16 * C::kPitch + n * 8) * 2, c0, c1, c2, c3);
+            mma_16816(acc1[n], x0, x1, x2, x3, c0, c1);
+            mma_16816(acc1[n + 1], x0, x1, x2, x3, c2, c3);
+            if constexpr (!kDQ) {
+              ldsm_x4_t(b2 + (ks * 16 * C::kPitch + n * 8) * 2, c0, c1, c2, c3);
+              mma_16816(acc2[n], y0, y1, y2, y3, c0, c1);
+              mma_16816(acc2[n + 1], y0, y1, y2, y3, c2, c3);
+            }
           }
         }
       }
+    };
+    products();
+    if constexpr (kFine) {
+      __syncthreads();  // the first terms are no longer read
+      products();
     }
     __syncthreads();  // the buffer, P and dS are no longer read
   }

@@ -39,6 +39,11 @@
 // waits for the statistics, then lets dQ's CTAs start (the statistics are
 // therefore complete for them too); dQ's last CTA waits for the dK/dV kernel
 // before it ends, so that whatever follows in the stream finds both done.
+//
+// kFine: P and dS go to the tensor core as two bf16 terms each, the rounded
+// value and the rounded rest, so that the gradients' only rounding that counts
+// is their own.  Three more products in ten: only small problems take it
+// (kBwFineSteps).
 // All waits are bounded.
 #pragma once
 
@@ -122,11 +127,27 @@ __device__ __forceinline__ void bwd_probs(const BwdParams& p, const uint32_t (&s
   }
 }
 
-// dS of 32 columns as bf16 from what bwd_probs left (p times the factor), dP
-// and the rows' delta.  A hidden score is an exact zero whatever dP is.
+// 32 fp32 values rounded to bf16 into TMEM columns [0, 16) at tm, and with
+// kFine what the rounding left into columns [32, 48).
+template <bool kFine>
+__device__ __forceinline__ void bwd_store_bf16(uint32_t tm, const f2 (&v)[16]) {
+  uint32_t w[16];
+#pragma unroll
+  for (int c = 0; c < 16; ++c) w[c] = pack_bf16_f2(v[c]);
+  tmem_st16(tm, w);
+  if constexpr (kFine) {
+#pragma unroll
+    for (int c = 0; c < 16; ++c)
+      w[c] = pack_bf16_f2(f2_sub(v[c], f2_pack(__uint_as_float(w[c] << 16),
+                                               __uint_as_float(w[c] & 0xffff0000u))));
+    tmem_st16(tm + 32, w);
+  }
+}
+
+// dS of 32 columns from what bwd_probs left (p times the factor), dP and the
+// rows' delta.  A hidden score is an exact zero whatever dP is.
 __device__ __forceinline__ void bwd_ds(const f2* keep, const uint32_t (&dp)[32], const f2 (&dl)[16],
-                                       bool masked, uint32_t (&pk)[16]) {
-  f2 d[16];
+                                       bool masked, f2 (&d)[16]) {
 #pragma unroll
   for (int c = 0; c < 16; ++c)
     d[c] = f2_mul(keep[c], f2_sub(f2_pack(__uint_as_float(dp[2 * c]), __uint_as_float(dp[2 * c + 1])),
@@ -140,8 +161,6 @@ __device__ __forceinline__ void bwd_ds(const f2* keep, const uint32_t (&dp)[32],
       d[c] = f2_pack(k0 == 0.f ? 0.f : a, k1 == 0.f ? 0.f : b);
     }
   }
-#pragma unroll
-  for (int c = 0; c < 16; ++c) pk[c] = pack_bf16_f2(d[c]);
 }
 
 // 32 floats of shared memory, the same for every lane, as pairs.
@@ -275,7 +294,7 @@ __device__ __forceinline__ uint64_t bwd_desc_n(uint32_t tile) {
 }
 
 // ------------------------------------------------------------------ dK, dV
-template <int DCH, bool kCap>
+template <int DCH, bool kCap, bool kFine>
 __global__ void __launch_bounds__(kBwThreads, 1)
     bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -468,9 +487,11 @@ __global__ void __launch_bounds__(kBwThreads, 1)
           if (!(ok = wait(p_half, J & 1))) break;
           tc_fence_after();
           bwd_issue_ts<0, 2>(leader, tmem + 256, tmem, dn + (J & 1) * kTile, idesc_o, j == 0);
+          if (kFine) bwd_issue_ts<0, 2>(leader, tmem + 256, tmem + 32, dn + (J & 1) * kTile, idesc_o, false);
           if (!(ok = wait(p_full, J & 1))) break;
           tc_fence_after();
           bwd_issue_ts<2, 4>(leader, tmem + 256, tmem, dn + (J & 1) * kTile, idesc_o, false);
+          if (kFine) bwd_issue_ts<2, 4>(leader, tmem + 256, tmem + 32, dn + (J & 1) * kTile, idesc_o, false);
           mma_commit_warp(leader, &do_empty[J & 1]);
           if (more) {
             bwd_issue_ss<DCH>(leader, tmem, kd, qk + sq_n * kTile, idesc_s, ksteps);
@@ -494,6 +515,8 @@ __global__ void __launch_bounds__(kBwThreads, 1)
           if (j + 1 < n && !(ok = wait(&s_full[(J + 1) & 1], ((J + 1) / 2) & 1))) break;
           tc_fence_after();
           bwd_issue_ts<0, 4>(leader, tmem + 384, tmem + 128, qn + sq_j * kTile, idesc_o, j == 0);
+          if (kFine)
+            bwd_issue_ts<0, 4>(leader, tmem + 384, tmem + 160, qn + sq_j * kTile, idesc_o, false);
           mma_commit_warp(leader, &q_empty[sq_j]);
           if (++sq_j == 3) sq_j = 0;
         }
@@ -563,16 +586,13 @@ __global__ void __launch_bounds__(kBwThreads, 1)
         f2 pr[16], fac[16];
         bwd_probs<kCap>(p, sv32, nl, pr, fac);
         if (need_mask) bwd_hide(pr, seen[g]);
-        uint32_t pk[16];
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          pk[c] = pack_bf16_f2(pr[c]);
-          keep[16 * g + c] = kCap ? f2_mul(pr[c], fac[c]) : pr[c];
-        }
-        tmem_st16(s_tm + 16 * g, pk);
+        for (int c = 0; c < 16; ++c) keep[16 * g + c] = kCap ? f2_mul(pr[c], fac[c]) : pr[c];
+        bwd_store_bf16<kFine>(s_tm + 16 * g, pr);
       };
+      if (kFine) tmem_ld32(s_tm + 32, b1);  // the rests go over these scores
       tmem_ld_wait();
-      tmem_ld32(s_tm + 32, b1);
+      if (!kFine) tmem_ld32(s_tm + 32, b1);
       probs(b0, 0);
       tmem_ld_wait();
       tmem_st_wait();
@@ -591,15 +611,15 @@ __global__ void __launch_bounds__(kBwThreads, 1)
       ok = __all_sync(0xffffffffu, mbar_wait(dp_full, par, kStatusTimeoutSoftmax));
       if (!ok) break;
       tc_fence_after();
-      uint32_t pk[16];
+      f2 ds[16];
       tmem_ld32(dp_tm, b0);
       tmem_ld32(dp_tm + 32, b1);
       tmem_ld_wait();
-      bwd_ds(keep, b0, dl, need_mask, pk);
-      tmem_st16(dp_tm, pk);
+      bwd_ds(keep, b0, dl, need_mask, ds);
+      bwd_store_bf16<kFine>(dp_tm, ds);
       bwd_load32(st + 160, dl);
-      bwd_ds(keep + 16, b1, dl, need_mask, pk);
-      tmem_st16(dp_tm + 16, pk);
+      bwd_ds(keep + 16, b1, dl, need_mask, ds);
+      bwd_store_bf16<kFine>(dp_tm + 16, ds);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -656,7 +676,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
 }
 
 // ------------------------------------------------------------------ dQ
-template <int DCH, bool kCap>
+template <int DCH, bool kCap, bool kFine>
 __global__ void __launch_bounds__(kBwThreads, 1)
     bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                   const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -825,6 +845,8 @@ __global__ void __launch_bounds__(kBwThreads, 1)
           if (!(ok = wait(&ds_full[J & 1], (J / 2) & 1))) break;
           tc_fence_after();
           bwd_issue_ts<0, 4>(leader, tmem + 384, tmem + 128 * (J & 1), kn + k_j * kTile, idesc_o, j == 0);
+          if (kFine)
+            bwd_issue_ts<0, 4>(leader, tmem + 384, tmem + 128 * (J & 1) + 32, kn + k_j * kTile, idesc_o, false);
           mma_commit_warp(leader, &k_empty[k_j]);
           if (++k_j == 3) k_j = 0;
           if (x < x_end && !(ok = issue_s())) break;
@@ -897,16 +919,16 @@ __global__ void __launch_bounds__(kBwThreads, 1)
       ok = __all_sync(0xffffffffu, mbar_wait(dp_full, J & 1, kStatusTimeoutSoftmax));
       if (!ok) break;
       tc_fence_after();
-      uint32_t pk[16];
+      f2 ds[16];
       tmem_ld32(tmem + lane_base + 256 + 64 * h, b0);
       tmem_ld32(tmem + lane_base + 288 + 64 * h, b1);
 #pragma unroll
       for (int c = 0; c < 16; ++c) row[c] = f2_pack(delta, delta);
       tmem_ld_wait();
-      bwd_ds(keep, b0, row, need_mask, pk);
-      tmem_st16(s_tm, pk);
-      bwd_ds(keep + 16, b1, row, need_mask, pk);
-      tmem_st16(s_tm + 16, pk);
+      bwd_ds(keep, b0, row, need_mask, ds);
+      bwd_store_bf16<kFine>(s_tm, ds);
+      bwd_ds(keep + 16, b1, row, need_mask, ds);
+      bwd_store_bf16<kFine>(s_tm + 16, ds);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();

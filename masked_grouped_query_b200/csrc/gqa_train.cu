@@ -82,6 +82,7 @@ struct BwdPlan {
   int tile;  // rows of a key or row tile: 128 (tcgen05) or 64
   long long key_tiles, row_tiles;
   int kv_splits, q_splits;
+  bool fine;
   size_t off_dk, off_dv, off_dq, bytes;
 };
 
@@ -104,6 +105,15 @@ int bwd_splits(long long items, long long steps, int tile) {
   return (int)(fit < most ? fit : most);
 }
 
+// Problems of at most this many steps (one per SM) take P and dS in two bf16
+// terms.  Their gradients' error, in the 2-norm, then is the outputs' rounding
+// alone, 1.7e-3; with one term it is 2.4e-3, and where few products make a
+// gradient up to twice the rounding.  Measured, microseconds with one and two
+// terms (captured calls): 23 and 27 (1, 128, 128, 4:1, 128), 16 and 20 (1, 512,
+// 512, 2:2, 128), less than the host takes to launch either; but 21 and 27 for
+// 512 steps (1, 1024, 1024, 8:8, 64), 1519 and 2159 for the largest case.
+constexpr long long kBwFineSteps = 148;
+
 BwdPlan bwd_plan(const BwdShape& s, bool may_split) {
   BwdPlan pl;
   pl.tile = s.head_dim > 128 ? 64 : 128;
@@ -117,6 +127,8 @@ BwdPlan bwd_plan(const BwdShape& s, bool may_split) {
     if (s.run == s.q_len && seen < rows) rows = seen;
     if (seen < keys) keys = seen;
   }
+  const long long steps = pl.key_tiles * (rows * s.runs_per_unit);
+  pl.fine = steps <= kBwFineSteps;
   pl.kv_splits = may_split ? bwd_splits(pl.key_tiles, rows * s.runs_per_unit, pl.tile) : 1;
   pl.q_splits = may_split ? bwd_splits(pl.row_tiles, keys, pl.tile) : 1;
   auto align = [](size_t x) { return (x + 255) & ~(size_t)255; };
@@ -149,19 +161,19 @@ int launch_after(const char* where, void (*kernel)(P...), long long grid, int th
   return e == cudaSuccess ? GQA_ATTN_OK : cuda_fail(where, e, GQA_ATTN_ERR_LAUNCH);
 }
 
-template <int KS>
+template <int KS, bool kFine>
 int launch_bwd_mma(const BwdParams& p, int device, cudaStream_t st) {
   using C = BwdMmaCfg<KS>;
   static bool done_kv[kMaxDevices], done_q[kMaxDevices];
-  int rc = allow_smem(bwd_mma_kernel<KS, false>, C::kSmemBytes, device, done_kv);
-  if (rc == GQA_ATTN_OK) rc = allow_smem(bwd_mma_kernel<KS, true>, C::kSmemBytes, device, done_q);
+  int rc = allow_smem(bwd_mma_kernel<KS, false, kFine>, C::kSmemBytes, device, done_kv);
+  if (rc == GQA_ATTN_OK) rc = allow_smem(bwd_mma_kernel<KS, true, kFine>, C::kSmemBytes, device, done_q);
   if (rc != GQA_ATTN_OK) return rc;
   const long long key_tiles = p.sh.units * ceil_div(p.sh.kv_len, kBmTile);
-  if ((rc = launch_after("launch(backward dK dV)", bwd_mma_kernel<KS, false>, key_tiles * p.kv_splits, kBmThreads,
+  if ((rc = launch_after("launch(backward dK dV)", bwd_mma_kernel<KS, false, kFine>, key_tiles * p.kv_splits, kBmThreads,
                          C::kSmemBytes, st, p)) != GQA_ATTN_OK)
     return rc;
   const long long row_tiles = p.sh.runs * ceil_div(p.sh.run, kBmTile);
-  return launch_after("launch(backward dQ)", bwd_mma_kernel<KS, true>, row_tiles * p.q_splits, kBmThreads,
+  return launch_after("launch(backward dQ)", bwd_mma_kernel<KS, true, kFine>, row_tiles * p.q_splits, kBmThreads,
                       C::kSmemBytes, st, p);
 }
 
@@ -183,12 +195,12 @@ int bwd_sm100_setup(K kernel, int bytes, int device, bool* done) {
   return allow_smem(kernel, bytes, device, done);
 }
 
-template <int DCH, bool kCap>
+template <int DCH, bool kCap, bool kFine>
 int launch_bwd_sm100(const BwdParams& p, int device, int sms, cudaStream_t st) {
   using C = BwdCfg<DCH>;
   static bool done_kv[kMaxDevices], done_q[kMaxDevices];
-  int rc = bwd_sm100_setup(bwd_dkdv_kernel<DCH, kCap>, C::kSmemBytes, device, done_kv);
-  if (rc == GQA_ATTN_OK) rc = bwd_sm100_setup(bwd_dq_kernel<DCH, kCap>, C::kSmemBytes, device, done_q);
+  int rc = bwd_sm100_setup(bwd_dkdv_kernel<DCH, kCap, kFine>, C::kSmemBytes, device, done_kv);
+  if (rc == GQA_ATTN_OK) rc = bwd_sm100_setup(bwd_dq_kernel<DCH, kCap, kFine>, C::kSmemBytes, device, done_q);
   if (rc != GQA_ATTN_OK) return rc;
   const BwdShape& s = p.sh;
   CUtensorMap q, dout, k, v, dq, dk, dv;
@@ -206,15 +218,24 @@ int launch_bwd_sm100(const BwdParams& p, int device, int sms, cudaStream_t st) {
       return rc;
   const long long key_tiles = s.units * ceil_div(s.kv_len, 128) * p.kv_splits;
   const long long row_tiles = s.runs * s.tiles * p.q_splits;
-  if ((rc = launch_after("launch(backward dK dV)", bwd_dkdv_kernel<DCH, kCap>,
+  if ((rc = launch_after("launch(backward dK dV)", bwd_dkdv_kernel<DCH, kCap, kFine>,
                          key_tiles < sms ? key_tiles : sms, kBwThreads, C::kSmemBytes, st, q, dout, k,
                          v, dk, dv, p)) != GQA_ATTN_OK)
     return rc;
   // Four CTAs per SM, one after the other, even out what the key tiles left
   // uneven (one SM's share at a time would keep it).
   const long long q_grid = row_tiles < 4LL * sms ? row_tiles : 4LL * sms;
-  return launch_after("launch(backward dQ)", bwd_dq_kernel<DCH, kCap>, q_grid, kBwThreads,
+  return launch_after("launch(backward dQ)", bwd_dq_kernel<DCH, kCap, kFine>, q_grid, kBwThreads,
                       C::kSmemBytes, st, q, dout, k, v, dq, p);
+}
+
+template <int DCH>
+int launch_bwd_sm100_d(const BwdParams& p, bool fine, int device, int sms, cudaStream_t st) {
+  if (fine)
+    return p.softcap ? launch_bwd_sm100<DCH, true, true>(p, device, sms, st)
+                     : launch_bwd_sm100<DCH, false, true>(p, device, sms, st);
+  return p.softcap ? launch_bwd_sm100<DCH, true, false>(p, device, sms, st)
+                   : launch_bwd_sm100<DCH, false, false>(p, device, sms, st);
 }
 
 // ------------------------------------------------------------------ rotary
@@ -336,15 +357,11 @@ int gqa_attn_bwd(const void* dout, const void* q, const void* k, const void* v, 
   // The tcgen05 kernels hold dK and dV of 128 columns each in TMEM next to the
   // scores: wider heads stay on mma.sync.
   if (head_dim > 128)
-    rc = launch_bwd_mma<16>(p, device, st);
+    rc = (pl.fine ? launch_bwd_mma<16, true> : launch_bwd_mma<16, false>)(p, device, st);
   else if (narrow_mma)
-    rc = launch_bwd_mma<8>(p, device, st);
-  else if (head_dim <= 64)
-    rc = p.softcap ? launch_bwd_sm100<1, true>(p, device, sms, st)
-                   : launch_bwd_sm100<1, false>(p, device, sms, st);
+    rc = (pl.fine ? launch_bwd_mma<8, true> : launch_bwd_mma<8, false>)(p, device, st);
   else
-    rc = p.softcap ? launch_bwd_sm100<2, true>(p, device, sms, st)
-                   : launch_bwd_sm100<2, false>(p, device, sms, st);
+    rc = (head_dim <= 64 ? launch_bwd_sm100_d<1> : launch_bwd_sm100_d<2>)(p, pl.fine, device, sms, st);
   if (rc != GQA_ATTN_OK || (pl.kv_splits == 1 && pl.q_splits == 1)) return rc;
   BwdJoin j;
   j.job[0] = {p.part_dk, p.dk, p.scale, pl.kv_splits, kv_len, s.units, pl.key_tiles};

@@ -98,6 +98,24 @@ def test_backward(case, dlse):
     assert mgq.status() & 0x1f == 0
 
 
+def steps(case):
+    """Key tiles times row tiles, heads apart (at least what the library counts)."""
+    b, lq, lk, hq, _, d = case[:6]
+    tile = 64 if d > 128 else 128
+    return b * hq * (-(-lq // tile)) * (-(-lk // tile))
+
+
+@pytest.mark.parametrize("case", [c for c in CASES if steps(c) <= 148], ids=str)
+def test_small_problems_keep_two_terms(case):
+    # At most 148 steps: P and dS in two bf16 terms.
+    t, kw = make(case, seed=13)
+    o, lse = mgq.attention_lse(t["q"], t["k"], t["v"], **kw)
+    want, bound = ref.backward(t["q"], t["k"], t["v"], o, lse, t["do"], None, inner=2.0 ** -16, **kw)
+    got = mgq.attention_backward(t["do"], t["q"], t["k"], t["v"], o, lse, **kw)
+    for n, g, w, b in zip(("dq", "dk", "dv"), got, want, bound):
+        ref.assert_within(n, g, w, b)
+
+
 def test_results_are_deterministic():
     t, kw = make((2, 700, 900, 8, 2, 128, True, 400, 30.0, 3), seed=2, dlse=True)
     o, lse = mgq.attention_lse(t["q"], t["k"], t["v"], **kw)

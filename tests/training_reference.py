@@ -1,7 +1,8 @@
 """64-bit references of the training operators and how far a kernel may be off.
 
 A rounding to bf16 is off by at most half a step, 2^-8 relative; the kernels
-round P and dS to bf16 for the tensor cores and every output once.  What is
+round P and dS to bf16 for the tensor cores (on small problems to two bf16
+terms, 2^-16 together) and every output once.  What is
 held in fp32 (products summed over head_dim, exponentials, the row
 statistics) is given 2^-18 of the sum of the magnitudes involved: 2^-24 a
 rounding, for the up to 256 / 16 + 16 partial sums and the approximate
@@ -71,8 +72,9 @@ def fold(x, group):
     return x.view(b, h // group, group, *x.shape[2:]).sum(2)
 
 
-def backward(q, k, v, o, lse, do, dlse, causal, window, softcap):
-    """fp64 gradients from the statistics given, and their bounds."""
+def backward(q, k, v, o, lse, do, dlse, causal, window, softcap, inner=U16):
+    """fp64 gradients from the statistics given, and their bounds; ``inner`` is
+    the relative rounding of P and dS."""
     f = forward(q, k, v, causal, window, softcap)
     do, o = do.double(), o.double()
     stat = lse.double()
@@ -91,8 +93,8 @@ def backward(q, k, v, o, lse, do, dlse, causal, window, softcap):
     finite = torch.where(torch.isinf(stat), torch.zeros_like(stat), stat).abs()[..., None]
     xmag = torch.where(f["see"], f["x"], torch.zeros_like(f["x"])).abs()
     ep = logit_error(f) + E32 * (1.0 + finite + xmag)
-    p_err = (U16 + ep) * p
-    ds_err = (U16 + ep) * ds.abs() + f["scale"] * p * E32 * dp_mag * chain \
+    p_err = (inner + ep) * p
+    ds_err = (inner + ep) * ds.abs() + f["scale"] * p * E32 * dp_mag * chain \
         + f["scale"] * p * (dp - delta).abs() * 1e-6
     g = f["group"]
     dq = ds @ f["k"]
