@@ -113,6 +113,16 @@ __global__ void __maxnreg__(kT ? 128 : 255)
   const int t_end = min(kr.t_count, t_begin + p.tiles_per_split);
   const int n_tiles = max(0, t_end - t_begin);
 
+  if constexpr (kLse) {
+    // Row blocks that see no key, most of a long prompt over few: zeros at once.
+    if (n_tiles == 0 && p.splits == 1) {
+      const long long row = (long long)unit * p.rows + r0;
+      uint4* o = reinterpret_cast<uint4*>(p.o + row * p.head_dim);  // head_dim % 8 == 0
+      for (int i = threadIdx.x; i < nr * p.head_dim / 8; i += kDecThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
+      for (int i = threadIdx.x; i < nr; i += kDecThreads) p.lse[row + i] = -INFINITY;
+      return;
+    }
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -529,6 +539,47 @@ __global__ void __maxnreg__(kT ? 128 : 255)
 
   const bool direct = p.splits == 1;
   const long long prow0 = (((long long)unit * p.row_blocks + rb) * p.splits + split) * p.block_rows;
+  if constexpr (kLse && !kT) {
+    // A warp per row: the row's weights once, two columns a lane.  (Element by
+    // element, as below, the many row blocks of a long prompt with wide heads
+    // spend half of their time here.)
+    for (int row = warp; row < nr; row += kDecComputeWarps) {
+      const float* rows_p = mrg + ((row >> 4) * 16 + (row & 15)) * (DP + 2);
+      const int step = wm_count * 16 * (DP + 2);
+      float M = -INFINITY;
+      for (int w = 0; w < wn_count; ++w) M = fmaxf(M, rows_p[w * step + DP]);
+      const float Mb = (M == -INFINITY) ? 0.f : M;
+      float f[kDecComputeWarps], L = 0.f;
+#pragma unroll
+      for (int w = 0; w < kDecComputeWarps; ++w) {
+        f[w] = w < wn_count ? ex2(rows_p[w * step + DP] - Mb) : 0.f;
+        if (w < wn_count) L += f[w] * rows_p[w * step + DP + 1];
+      }
+      for (int d = 2 * lane; d < D; d += 64) {
+        float a = 0.f, b = 0.f;
+#pragma unroll
+        for (int w = 0; w < kDecComputeWarps; ++w)
+          if (w < wn_count) {
+            const float2 x = *reinterpret_cast<const float2*>(rows_p + w * step + d);
+            a += f[w] * x.x;
+            b += f[w] * x.y;
+          }
+        a = L > 0.f ? a / L : 0.f;
+        b = L > 0.f ? b / L : 0.f;
+        if (direct)
+          *reinterpret_cast<uint32_t*>(p.o + ((long long)unit * p.rows + r0 + row) * D + d) = pack_bf16(a, b);
+        else
+          *reinterpret_cast<float2*>(p.part_o + (prow0 + row) * D + d) = make_float2(a, b);
+      }
+      if (lane == 0) {
+        if (direct)
+          p.lse[(long long)unit * p.rows + r0 + row] =
+              L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+        else
+          p.part_lse[prow0 + row] = L > 0.f ? M + log2f(L) : -INFINITY;
+      }
+    }
+  } else
   for (int idx = threadIdx.x; idx < nr * D; idx += kDecComputeWarps * 32) {
     const int row = idx / D, d = idx - (idx / D) * D;
     const int rwm = row >> 4, r = row & 15;

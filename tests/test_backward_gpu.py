@@ -38,6 +38,7 @@ CASES = [
     (1, 1100, 1300, 1, 1, 104, True, None, None, 1),   # both, of uneven length
     (1, 1400, 90, 2, 1, 200, True, None, None, 1),     # wide heads
     (1, 5, 2100, 2, 1, 256, False, 1500, 20.0, 1),
+    (1, 700, 16, 16, 4, 256, True, 26, None, 4),       # most rows of wide heads empty
 ]
 
 
