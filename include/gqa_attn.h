@@ -1,6 +1,7 @@
 /*
- * gqa_attn.h -- C ABI of libgqa_attn.so: masked grouped-query attention
- * forward pass on NVIDIA B200 (sm_100a).
+ * gqa_attn.h -- C ABI of libgqa_attn.so: masked grouped-query attention on
+ * NVIDIA B200 (sm_100a): forward pass, KV cache, backward pass and rotary
+ * positions.
  *
  * Operation ("TPU v6e Masked GQA Kernel Optimization", sections "What You
  * Have" and "What You Submit"): for bf16 q (batch, num_q_heads, q_len,
@@ -123,7 +124,8 @@ int gqa_attn_fwd(const void* q, const void* k, const void* v, void* o, int batch
  * lse: device pointer, [batch][num_q_heads][q_len] fp32, 16-byte aligned,
  * overlapping no other argument; the caller owns it.  Everything else,
  * the workspace and the rules for CUDA graphs among it, is as for
- * gqa_attn_fwd.  The kernels behind this entry point take exponentials and
+ * gqa_attn_fwd: in particular, graphs captured on one stream share that
+ * stream's workspace, and replay one after the other.  The kernels behind this entry point take exponentials and
  * tanh more exactly than gqa_attn_fwd's, so o may differ from its o in the
  * last bit.
  */
