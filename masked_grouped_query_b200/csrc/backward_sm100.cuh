@@ -539,131 +539,131 @@ __global__ void __launch_bounds__(kBwThreads, 1)
     int i = bwd_item(s, 0);
     Item it = item_at(i);
     for (int kk = 1; i < items && ok; ++kk) {
-    const int key = it.k0 + quarter * 32 + lane;
-    // Queries that see this lane's key: [qlo, qhi] (none past kv_len).
-    int qlo, qhi;
-    bwd_query_range(s, key, key, qlo, qhi);
-    if (key >= s.kv_len) qhi = -1;
-    int t = it.t;
-    for (int j = 0; j < it.n; ++j, ++J) {
-      const int r0 = t * 128, nr = min(128, s.run - r0);
-      const bool need_mask = bwd_need_mask(s, ms, r0, nr, it.k0, 128);
-      const uint32_t par = J & 1, dpar = (J / 2) & 1;
-      f2 keep[32];
-      const float* st = stats + par * 256 + 64 * h;
-      f2 nl[16];
-      ok = __all_sync(0xffffffffu, mbar_wait(&st_full[par], dpar, kStatusTimeoutSoftmax));
-      if (!ok) break;
-      bwd_load32(st, nl);
-      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[par], dpar, kStatusTimeoutSoftmax));
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t b0[32], b1[32];
-      tmem_ld32(s_tm, b0);
-      uint32_t seen[2] = {0u, 0u};  // this lane's key by the columns of its half
-      if (need_mask) {
-        const int c0 = r0 + 64 * h;
-        if (s.run == s.q_len) {
-          seen[0] = bwd_bits(qlo - c0, qhi - c0);
-          seen[1] = bwd_bits(qlo - c0 - 32, qhi - c0 - 32);
-        } else {  // several heads in the tile: query by query
-          int qi = c0 % s.q_len;
+      const int key = it.k0 + quarter * 32 + lane;
+      // Queries that see this lane's key: [qlo, qhi] (none past kv_len).
+      int qlo, qhi;
+      bwd_query_range(s, key, key, qlo, qhi);
+      if (key >= s.kv_len) qhi = -1;
+      int t = it.t;
+      for (int j = 0; j < it.n; ++j, ++J) {
+        const int r0 = t * 128, nr = min(128, s.run - r0);
+        const bool need_mask = bwd_need_mask(s, ms, r0, nr, it.k0, 128);
+        const uint32_t par = J & 1, dpar = (J / 2) & 1;
+        f2 keep[32];
+        const float* st = stats + par * 256 + 64 * h;
+        f2 nl[16];
+        ok = __all_sync(0xffffffffu, mbar_wait(&st_full[par], dpar, kStatusTimeoutSoftmax));
+        if (!ok) break;
+        bwd_load32(st, nl);
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[par], dpar, kStatusTimeoutSoftmax));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t b0[32], b1[32];
+        tmem_ld32(s_tm, b0);
+        uint32_t seen[2] = {0u, 0u};  // this lane's key by the columns of its half
+        if (need_mask) {
+          const int c0 = r0 + 64 * h;
+          if (s.run == s.q_len) {
+            seen[0] = bwd_bits(qlo - c0, qhi - c0);
+            seen[1] = bwd_bits(qlo - c0 - 32, qhi - c0 - 32);
+          } else {  // several heads in the tile: query by query
+            int qi = c0 % s.q_len;
 #pragma unroll 1
-          for (int c = 0; c < 32; ++c) {
-            if (qi >= qlo && qi <= qhi) seen[0] |= 1u << c;
-            if (++qi == s.q_len) qi = 0;
-          }
+            for (int c = 0; c < 32; ++c) {
+              if (qi >= qlo && qi <= qhi) seen[0] |= 1u << c;
+              if (++qi == s.q_len) qi = 0;
+            }
 #pragma unroll 1
-          for (int c = 0; c < 32; ++c) {
-            if (qi >= qlo && qi <= qhi) seen[1] |= 1u << c;
-            if (++qi == s.q_len) qi = 0;
+            for (int c = 0; c < 32; ++c) {
+              if (qi >= qlo && qi <= qhi) seen[1] |= 1u << c;
+              if (++qi == s.q_len) qi = 0;
+            }
           }
         }
-      }
-      // P of columns 32 g .. 32 g + 31 of this half, into TMEM columns
-      // [16 g, 16 g + 16) of it, whose scores have been read.
-      auto probs = [&](const uint32_t(&sv32)[32], int g) {
-        f2 pr[16], fac[16];
-        bwd_probs<kCap>(p, sv32, nl, pr, fac);
-        if (need_mask) bwd_hide(pr, seen[g]);
+        // P of columns 32 g .. 32 g + 31 of this half, into TMEM columns
+        // [16 g, 16 g + 16) of it, whose scores have been read.
+        auto probs = [&](const uint32_t(&sv32)[32], int g) {
+          f2 pr[16], fac[16];
+          bwd_probs<kCap>(p, sv32, nl, pr, fac);
+          if (need_mask) bwd_hide(pr, seen[g]);
 #pragma unroll
-        for (int c = 0; c < 16; ++c) keep[16 * g + c] = kCap ? f2_mul(pr[c], fac[c]) : pr[c];
-        bwd_store_bf16<kFine>(s_tm + 16 * g, pr);
-      };
-      if (kFine) tmem_ld32(s_tm + 32, b1);  // the rests go over these scores
-      tmem_ld_wait();
-      if (!kFine) tmem_ld32(s_tm + 32, b1);
-      probs(b0, 0);
-      tmem_ld_wait();
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_half);
-      bwd_load32(st + 32, nl);
-      probs(b1, 1);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full);
+          for (int c = 0; c < 16; ++c) keep[16 * g + c] = kCap ? f2_mul(pr[c], fac[c]) : pr[c];
+          bwd_store_bf16<kFine>(s_tm + 16 * g, pr);
+        };
+        if (kFine) tmem_ld32(s_tm + 32, b1);  // the rests go over these scores
+        tmem_ld_wait();
+        if (!kFine) tmem_ld32(s_tm + 32, b1);
+        probs(b0, 0);
+        tmem_ld_wait();
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_half);
+        bwd_load32(st + 32, nl);
+        probs(b1, 1);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
 
-      f2 dl[16];
-      bwd_load32(st + 128, dl);
-      ok = __all_sync(0xffffffffu, mbar_wait(dp_full, par, kStatusTimeoutSoftmax));
-      if (!ok) break;
-      tc_fence_after();
-      f2 ds[16];
-      tmem_ld32(dp_tm, b0);
-      tmem_ld32(dp_tm + 32, b1);
-      tmem_ld_wait();
-      bwd_ds(keep, b0, dl, need_mask, ds);
-      bwd_store_bf16<kFine>(dp_tm, ds);
-      bwd_load32(st + 160, dl);
-      bwd_ds(keep + 16, b1, dl, need_mask, ds);
-      bwd_store_bf16<kFine>(dp_tm + 16, ds);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(ds_full);
-        mbar_arrive(&st_empty[par]);
-        if (j + 1 < it.n) mbar_arrive(&do_empty[par]);  // the last slot holds the output boxes first
+        f2 dl[16];
+        bwd_load32(st + 128, dl);
+        ok = __all_sync(0xffffffffu, mbar_wait(dp_full, par, kStatusTimeoutSoftmax));
+        if (!ok) break;
+        tc_fence_after();
+        f2 ds[16];
+        tmem_ld32(dp_tm, b0);
+        tmem_ld32(dp_tm + 32, b1);
+        tmem_ld_wait();
+        bwd_ds(keep, b0, dl, need_mask, ds);
+        bwd_store_bf16<kFine>(dp_tm, ds);
+        bwd_load32(st + 160, dl);
+        bwd_ds(keep + 16, b1, dl, need_mask, ds);
+        bwd_store_bf16<kFine>(dp_tm + 16, ds);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(ds_full);
+          mbar_arrive(&st_empty[par]);
+          if (j + 1 < it.n) mbar_arrive(&do_empty[par]);  // the last slot holds the output boxes first
+        }
+        if (++t == it.first + it.count) t = it.first;
       }
-      if (++t == it.first + it.count) t = it.first;
-    }
-    if (!ok) break;
-    const int next = bwd_item(s, kk);
-    const Item next_it = item_at(next);  // ahead of the wait: divisions
-    if (it.n > 0) {
-      ok = __all_sync(0xffffffffu, mbar_wait(o_done, busy & 1, kStatusTimeoutEpilogue));
       if (!ok) break;
-      ++busy;
-      tc_fence_after();
-    }
-    // Warpgroup 0 stores dV, warpgroup 1 dK.  The next item's first products
-    // into them follow this thread's next P and dS arrivals.
-    const int row0 = it.k0 + quarter * 32;
-    if (splits > 1) {
-      const int d_pad = (s.head_dim + 15) / 16 * 16;
-      bwd_store_part((h ? p.part_dk : p.part_dv) + (long long)i * 128 * d_pad,
-                     tmem + lane_base + 256 + 128 * h, 0, d_pad, quarter * 32 + lane, it.n == 0);
-      if (lane == 0 && it.n > 0) mbar_arrive(&do_empty[(J - 1) & 1]);
-    } else if (it.n == 0) {
-      if (row0 < s.kv_len)
-        bwd_store_zeros((h ? p.dk : p.dv) + ((long long)it.unit * s.kv_len + row0) * s.head_dim,
-                        min(32, s.kv_len - row0), s.head_dim, lane);
-    } else {
-      uint8_t* stage = C::stage(smem, J - 1) + (warp - 4) * 4096;
+      const int next = bwd_item(s, kk);
+      const Item next_it = item_at(next);  // ahead of the wait: divisions
+      if (it.n > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(o_done, busy & 1, kStatusTimeoutEpilogue));
+        if (!ok) break;
+        ++busy;
+        tc_fence_after();
+      }
+      // Warpgroup 0 stores dV, warpgroup 1 dK.  The next item's first products
+      // into them follow this thread's next P and dS arrivals.
+      const int row0 = it.k0 + quarter * 32;
+      if (splits > 1) {
+        const int d_pad = (s.head_dim + 15) / 16 * 16;
+        bwd_store_part((h ? p.part_dk : p.part_dv) + (long long)i * 128 * d_pad,
+                       tmem + lane_base + 256 + 128 * h, 0, d_pad, quarter * 32 + lane, it.n == 0);
+        if (lane == 0 && it.n > 0) mbar_arrive(&do_empty[(J - 1) & 1]);
+      } else if (it.n == 0) {
+        if (row0 < s.kv_len)
+          bwd_store_zeros((h ? p.dk : p.dv) + ((long long)it.unit * s.kv_len + row0) * s.head_dim,
+                          min(32, s.kv_len - row0), s.head_dim, lane);
+      } else {
+        uint8_t* stage = C::stage(smem, J - 1) + (warp - 4) * 4096;
 #pragma unroll 1
-      for (int c0 = 0; c0 < s.head_dim && row0 < s.kv_len; c0 += 64)
-        bwd_store_box(h ? &tm_dk : &tm_dv, stage, tmem + lane_base + 256 + 128 * h + c0, c0, row0,
-                      it.unit, h ? p.scale : 1.f, c0 > 0, lane);
-      if (lane == 0) {
-        bulk_wait_read();  // the slot goes back to the loader
-        mbar_arrive(&do_empty[(J - 1) & 1]);
+        for (int c0 = 0; c0 < s.head_dim && row0 < s.kv_len; c0 += 64)
+          bwd_store_box(h ? &tm_dk : &tm_dv, stage, tmem + lane_base + 256 + 128 * h + c0, c0, row0,
+                        it.unit, h ? p.scale : 1.f, c0 > 0, lane);
+        if (lane == 0) {
+          bulk_wait_read();  // the slot goes back to the loader
+          mbar_arrive(&do_empty[(J - 1) & 1]);
+        }
       }
-    }
-    i = next;
-    it = next_it;
+      i = next;
+      it = next_it;
     }
     if (lane == 0) bulk_wait_all();  // stores done before the CTA exits
   }
@@ -882,93 +882,93 @@ __global__ void __launch_bounds__(kBwThreads, 1)
     int i = bwd_item(s, 0);
     Item it = item_at(i);
     for (int kk = 1; i < items && ok; ++kk) {
-    const float* st = p.stats + ((long long)it.run * s.tiles + it.tile) * 256;
-    const float nlse = st[r], delta = st[128 + r];
-    int lo = 0, hi = -1;
-    if (r < it.nr) {
-      const int qpos = s.kv_len - s.q_len + (it.r0 + r) % s.q_len;
-      lo = first_key(ms, qpos);
-      hi = last_key(ms, qpos);
-    }
-    for (int j = 0; j < it.kr.t_count; ++j, ++J) {
-      const int key0 = (it.kr.t_first + j) * 128;
-      const bool need_mask = !(key0 >= it.kr.all_lo && key0 + 127 <= it.kr.all_hi);
-      const int c0 = key0 + 64 * h;
-      const uint32_t s_tm = tmem + lane_base + 128 * (J & 1) + 64 * h;
-      f2 keep[32];
-      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[J & 1], (J / 2) & 1, kStatusTimeoutSoftmax));
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t b0[32], b1[32];
-      f2 row[16];
-      auto probs = [&](const uint32_t(&sv32)[32], int g) {
-        f2 pr[16], fac[16];
-#pragma unroll
-        for (int c = 0; c < 16; ++c) row[c] = f2_pack(nlse, nlse);
-        bwd_probs<kCap>(p, sv32, row, pr, fac);
-        if (need_mask) bwd_hide(pr, bwd_bits(lo - c0 - 32 * g, hi - c0 - 32 * g));
-#pragma unroll
-        for (int c = 0; c < 16; ++c) keep[16 * g + c] = kCap ? f2_mul(pr[c], fac[c]) : pr[c];
-      };
-      tmem_ld32(s_tm, b0);
-      tmem_ld_wait();
-      tmem_ld32(s_tm + 32, b1);
-      probs(b0, 0);
-      tmem_ld_wait();
-      probs(b1, 1);
-      ok = __all_sync(0xffffffffu, mbar_wait(dp_full, J & 1, kStatusTimeoutSoftmax));
-      if (!ok) break;
-      tc_fence_after();
-      f2 ds[16];
-      tmem_ld32(tmem + lane_base + 256 + 64 * h, b0);
-      tmem_ld32(tmem + lane_base + 288 + 64 * h, b1);
-#pragma unroll
-      for (int c = 0; c < 16; ++c) row[c] = f2_pack(delta, delta);
-      tmem_ld_wait();
-      bwd_ds(keep, b0, row, need_mask, ds);
-      bwd_store_bf16<kFine>(s_tm, ds);
-      bwd_ds(keep + 16, b1, row, need_mask, ds);
-      bwd_store_bf16<kFine>(s_tm + 16, ds);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&ds_full[J & 1]);
-        // The last slot holds the output boxes first.
-        if (j + 1 < it.kr.t_count) mbar_arrive(&v_empty[J & 1]);
+      const float* st = p.stats + ((long long)it.run * s.tiles + it.tile) * 256;
+      const float nlse = st[r], delta = st[128 + r];
+      int lo = 0, hi = -1;
+      if (r < it.nr) {
+        const int qpos = s.kv_len - s.q_len + (it.r0 + r) % s.q_len;
+        lo = first_key(ms, qpos);
+        hi = last_key(ms, qpos);
       }
-    }
-    if (!ok) break;
-    const int next = bwd_item(s, kk);
-    const Item next_it = item_at(next);  // ahead of the wait: divisions
-    if (it.kr.t_count > 0) {
-      ok = __all_sync(0xffffffffu, mbar_wait(o_done, busy & 1, kStatusTimeoutEpilogue));
-      if (!ok) break;
-      ++busy;
-      tc_fence_after();
-    }
-    // Each warpgroup stores its half of the columns.
-    const int rows = it.nr - quarter * 32;
-    if (splits > 1) {
-      const int d_pad = (s.head_dim + 15) / 16 * 16;
-      bwd_store_part(p.part_dq + (long long)it.part * 128 * d_pad, tmem + lane_base + 384, 64 * h,
-                     min(64 * h + 64, d_pad), r, it.kr.t_count == 0);
-      if (lane == 0 && it.kr.t_count > 0) mbar_arrive(&v_empty[(J - 1) & 1]);
-    } else if (it.kr.t_count == 0) {
-      if (rows > 0 && h == 0)
-        bwd_store_zeros(p.dq + ((long long)it.run * s.run + it.r0 + quarter * 32) * s.head_dim,
-                        min(32, rows), s.head_dim, lane);
-    } else {
-      if (rows > 0 && 64 * h < s.head_dim)
-        bwd_store_box(&tm_dq, C::stage(smem, J - 1) + (warp - 4) * 4096, tmem + lane_base + 384 + 64 * h,
-                      64 * h, it.r0 + quarter * 32, it.run, p.scale, false, lane);
-      if (lane == 0) {
-        bulk_wait_read();  // the slot goes back to the loader
-        mbar_arrive(&v_empty[(J - 1) & 1]);
+      for (int j = 0; j < it.kr.t_count; ++j, ++J) {
+        const int key0 = (it.kr.t_first + j) * 128;
+        const bool need_mask = !(key0 >= it.kr.all_lo && key0 + 127 <= it.kr.all_hi);
+        const int c0 = key0 + 64 * h;
+        const uint32_t s_tm = tmem + lane_base + 128 * (J & 1) + 64 * h;
+        f2 keep[32];
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[J & 1], (J / 2) & 1, kStatusTimeoutSoftmax));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t b0[32], b1[32];
+        f2 row[16];
+        auto probs = [&](const uint32_t(&sv32)[32], int g) {
+          f2 pr[16], fac[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) row[c] = f2_pack(nlse, nlse);
+          bwd_probs<kCap>(p, sv32, row, pr, fac);
+          if (need_mask) bwd_hide(pr, bwd_bits(lo - c0 - 32 * g, hi - c0 - 32 * g));
+#pragma unroll
+          for (int c = 0; c < 16; ++c) keep[16 * g + c] = kCap ? f2_mul(pr[c], fac[c]) : pr[c];
+        };
+        tmem_ld32(s_tm, b0);
+        tmem_ld_wait();
+        tmem_ld32(s_tm + 32, b1);
+        probs(b0, 0);
+        tmem_ld_wait();
+        probs(b1, 1);
+        ok = __all_sync(0xffffffffu, mbar_wait(dp_full, J & 1, kStatusTimeoutSoftmax));
+        if (!ok) break;
+        tc_fence_after();
+        f2 ds[16];
+        tmem_ld32(tmem + lane_base + 256 + 64 * h, b0);
+        tmem_ld32(tmem + lane_base + 288 + 64 * h, b1);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) row[c] = f2_pack(delta, delta);
+        tmem_ld_wait();
+        bwd_ds(keep, b0, row, need_mask, ds);
+        bwd_store_bf16<kFine>(s_tm, ds);
+        bwd_ds(keep + 16, b1, row, need_mask, ds);
+        bwd_store_bf16<kFine>(s_tm + 16, ds);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&ds_full[J & 1]);
+          // The last slot holds the output boxes first.
+          if (j + 1 < it.kr.t_count) mbar_arrive(&v_empty[J & 1]);
+        }
       }
-    }
-    i = next;
-    it = next_it;
+      if (!ok) break;
+      const int next = bwd_item(s, kk);
+      const Item next_it = item_at(next);  // ahead of the wait: divisions
+      if (it.kr.t_count > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(o_done, busy & 1, kStatusTimeoutEpilogue));
+        if (!ok) break;
+        ++busy;
+        tc_fence_after();
+      }
+      // Each warpgroup stores its half of the columns.
+      const int rows = it.nr - quarter * 32;
+      if (splits > 1) {
+        const int d_pad = (s.head_dim + 15) / 16 * 16;
+        bwd_store_part(p.part_dq + (long long)it.part * 128 * d_pad, tmem + lane_base + 384, 64 * h,
+                       min(64 * h + 64, d_pad), r, it.kr.t_count == 0);
+        if (lane == 0 && it.kr.t_count > 0) mbar_arrive(&v_empty[(J - 1) & 1]);
+      } else if (it.kr.t_count == 0) {
+        if (rows > 0 && h == 0)
+          bwd_store_zeros(p.dq + ((long long)it.run * s.run + it.r0 + quarter * 32) * s.head_dim,
+                          min(32, rows), s.head_dim, lane);
+      } else {
+        if (rows > 0 && 64 * h < s.head_dim)
+          bwd_store_box(&tm_dq, C::stage(smem, J - 1) + (warp - 4) * 4096, tmem + lane_base + 384 + 64 * h,
+                        64 * h, it.r0 + quarter * 32, it.run, p.scale, false, lane);
+        if (lane == 0) {
+          bulk_wait_read();  // the slot goes back to the loader
+          mbar_arrive(&v_empty[(J - 1) & 1]);
+        }
+      }
+      i = next;
+      it = next_it;
     }
     if (lane == 0) bulk_wait_all();  // stores done before the CTA exits
   }
