@@ -118,16 +118,18 @@ int gqa_attn_fwd(const void* q, const void* k, const void* v, void* o, int batch
 /*
  * gqa_attn_fwd_lse -- gqa_attn_fwd that also returns every row's log-sum-exp,
  * lse[b][h][i] = ln(sum over visible keys of e^x) in fp32 (-inf for a row
- * without a visible key; o is zero there).  The backward pass reads it, and
- * it merges results over disjoint sets of keys: o = sum_s e^(lse_s - lse) o_s.
+ * without a visible key; o is zero there).  A row with a NaN logit, or with an
+ * infinite one and no softcap, gets NaN in both: it is not taken for empty.
+ * The backward pass reads lse, and it merges results over disjoint sets of
+ * keys: o = sum_s e^(lse_s - lse) o_s.
  *
  * lse: device pointer, [batch][num_q_heads][q_len] fp32, 16-byte aligned,
  * overlapping no other argument; the caller owns it.  Everything else,
  * the workspace and the rules for CUDA graphs among it, is as for
  * gqa_attn_fwd: in particular, graphs captured on one stream share that
- * stream's workspace, and replay one after the other.  The kernels behind this entry point take exponentials and
- * tanh more exactly than gqa_attn_fwd's, so o may differ from its o in the
- * last bit.
+ * stream's workspace, and replay one after the other.  The kernels behind
+ * this entry point take exponentials and tanh more exactly than
+ * gqa_attn_fwd's, so o may differ from its o in the last bit.
  */
 int gqa_attn_fwd_lse(const void* q, const void* k, const void* v, void* o, float* lse, int batch,
                      int q_len, int kv_len, int num_q_heads, int num_kv_heads, int head_dim,

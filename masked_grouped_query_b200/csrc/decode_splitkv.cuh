@@ -86,7 +86,8 @@ struct DecodeCfg {
 // accumulator needs half the registers (two CTAs per SM).
 //
 // kLse: also returns every row's log-sum-exp in fp32, with an accurate tanh
-// in place of the hardware's (5e-4 relative).
+// in place of the hardware's (5e-4 relative).  A row is empty when its sum is
+// zero; a sum that is NaN goes on to o and to the statistic.
 template <int KS, bool kT, bool kDeep = false, bool kLse = false>
 __global__ void __maxnreg__(kT ? 128 : 255)
     decode_splitkv_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -564,8 +565,8 @@ __global__ void __maxnreg__(kT ? 128 : 255)
             a += f[w] * x.x;
             b += f[w] * x.y;
           }
-        a = L > 0.f ? a / L : 0.f;
-        b = L > 0.f ? b / L : 0.f;
+        a = L != 0.f ? a / L : 0.f;
+        b = L != 0.f ? b / L : 0.f;
         if (direct)
           *reinterpret_cast<uint32_t*>(p.o + ((long long)unit * p.rows + r0 + row) * D + d) = pack_bf16(a, b);
         else
@@ -574,9 +575,9 @@ __global__ void __maxnreg__(kT ? 128 : 255)
       if (lane == 0) {
         if (direct)
           p.lse[(long long)unit * p.rows + r0 + row] =
-              L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+              L != 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
         else
-          p.part_lse[prow0 + row] = L > 0.f ? M + log2f(L) : -INFINITY;
+          p.part_lse[prow0 + row] = L != 0.f ? M + log2f(L) : -INFINITY;
       }
     }
   } else
@@ -594,15 +595,16 @@ __global__ void __maxnreg__(kT ? 128 : 255)
       L += f * row_p[DP + 1];
       O += f * row_p[d];
     }
-    const float o_val = L > 0.f ? O / L : 0.f;
+    const bool some = kLse ? L != 0.f : L > 0.f;
+    const float o_val = some ? O / L : 0.f;
     if (direct) {
       p.o[((long long)unit * p.rows + r0 + row) * D + d] = __float2bfloat16_rn(o_val);
       if (kLse && d == 0)
         p.lse[(long long)unit * p.rows + r0 + row] =
-            L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+            some ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
     } else {
       p.part_o[(prow0 + row) * D + d] = o_val;
-      if (d == 0) p.part_lse[prow0 + row] = L > 0.f ? M + log2f(L) : -INFINITY;
+      if (d == 0) p.part_lse[prow0 + row] = some ? M + log2f(L) : -INFINITY;
     }
   }
   __syncthreads();  // (B) pairs with the loader's second barrier
@@ -627,18 +629,20 @@ __global__ void __maxnreg__(kT ? 128 : 255)
     float M = -INFINITY;
     for (int s = 0; s < p.splits; ++s)
       M = fmaxf(M, __ldcg(&p.part_lse[pbase + (long long)s * p.block_rows + row]));
+    // fmaxf passes over a NaN: with statistics wanted it has to reach the sum.
+    const float Mb = kLse && M == -INFINITY ? 0.f : M;
     float L = 0.f;
     for (int s = 0; s < p.splits; ++s) {
-      const float f = M == -INFINITY
+      const float f = !kLse && M == -INFINITY
                           ? 0.f
-                          : ex2(__ldcg(&p.part_lse[pbase + (long long)s * p.block_rows + row]) - M);
+                          : ex2(__ldcg(&p.part_lse[pbase + (long long)s * p.block_rows + row]) - Mb);
       wgt[s * nr + row] = f;
       L += f;
     }
-    const float inv = L > 0.f ? 1.0f / L : 0.f;
+    const float inv = (kLse ? L != 0.f : L > 0.f) ? 1.0f / L : 0.f;
     if (kLse)
       p.lse[(long long)unit * p.rows + r0 + row] =
-          L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+          L != 0.f ? (Mb + log2f(L)) * 0.69314718055994531f : -INFINITY;
     for (int s = 0; s < p.splits; ++s) wgt[s * nr + row] *= inv;
   }
   asm volatile("bar.sync 1, %0;" ::"r"(kDecComputeWarps * 32) : "memory");

@@ -123,9 +123,9 @@ struct PrefillParams {
 };
 
 // Natural-log log-sum-exp of a row from its base and sum in log2 units
-// (-inf for a row without a visible key).
+// (-inf for a row without a visible key, whose sum is zero; NaN stays NaN).
 __device__ __forceinline__ float row_lse(float m, float l) {
-  return l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 // cap_out * tanh(x * cap_in) + c for a pair with |x * cap_in| <= 1, as x Q(x^2)
@@ -1012,7 +1012,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       // still goes there (with ok = false) instead of leaving at once.
       // Fixed-base softcap: a row without a visible key keeps m = -inf.
       if constexpr (kCapDeg == 3)
-        if (!(l > 0.f)) m = -INFINITY;
+        if (kLse ? l == 0.f : !(l > 0.f)) m = -INFINITY;
+      // A row whose sum is NaN (a NaN or infinite logit, which a maximum may
+      // not show) takes any finite base, so that it is not held for empty.
+      if constexpr (kLse)
+        if (l != l) m = 0.f;
       const bool pair_x = kSplit && it.paired;
       if (!ok && !pair_x) break;
       // ---- epilogue.  The next item's first P.V of this tile may overwrite
@@ -1058,7 +1062,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       if constexpr (!kSplit) {
         if (ti.nrows > 0 && quarter * 32 < ti.nrows) {
           const bool have = act > 0;  // warp-uniform
-          const bool live = have && m != -INFINITY && l > 0.f;
+          const bool live = have && (kLse ? l != 0.f : m != -INFINITY && l > 0.f);
           const float inv = live ? 1.0f / l : 0.f;
           if constexpr (kLse)
             if (r < ti.nrows)
@@ -1219,7 +1223,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                     M = mb8;
                   }
                 }
-                const float inv = Ls > 0.f ? 1.0f / Ls : 0.f;
+                const float inv = (kLse ? Ls != 0.f : Ls > 0.f) ? 1.0f / Ls : 0.f;
                 if (write_lse && row < wt.nrows)
                   p.lse[(long long)it.unit * p.rows + wt.row0 + row] = row_lse(M, Ls);
                 __nv_bfloat16* orow =
