@@ -415,15 +415,14 @@ __global__ void __launch_bounds__(kBmThreads, 1) bwd_mma_kernel(const BwdParams 
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int qr = kDQ ? m0 + g + 8 * (e >> 1) : n0 + n * 8 + 2 * t4 + (e & 1);
-        float t = 0.f, y;
+        float slope = 1.f, y;
         if (p.softcap) {
-          t = tanh_accurate(sc[n][e] * p.cap_in);
-          y = p.cap_out * t;
+          y = p.cap_out * tanh_accurate(sc[n][e] * p.cap_in, slope);
         } else {
           y = sc[n][e] * p.logit_scale;
         }
         sc[n][e] = ex2(y + st[qr]);
-        dp[n][e] = sc[n][e] * (dp[n][e] - st[64 + qr]) * (1.f - t * t);
+        dp[n][e] = sc[n][e] * (dp[n][e] - st[64 + qr]) * slope;
       }
     if (need_mask) {
 #pragma unroll

@@ -118,10 +118,11 @@ __device__ __forceinline__ void bwd_probs(const BwdParams& p, const uint32_t (&s
     } else {
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
-        const float a = tanh_large(__uint_as_float(s[2 * c]) * p.cap_in);
-        const float b = tanh_large(__uint_as_float(s[2 * c + 1]) * p.cap_in);
+        float fa, fb;
+        const float a = tanh_large(__uint_as_float(s[2 * c]) * p.cap_in, fa);
+        const float b = tanh_large(__uint_as_float(s[2 * c + 1]) * p.cap_in, fb);
         pr[c] = exp2_mufu_x2(f2_fma(co, f2_pack(a, b), nl[c]));
-        fac[c] = f2_pack(fmaf(-a, a, 1.f), fmaf(-b, b, 1.f));
+        fac[c] = f2_pack(fa, fb);
       }
     }
   }

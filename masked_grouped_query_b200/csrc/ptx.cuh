@@ -465,6 +465,21 @@ __device__ __forceinline__ float tanh_large(float y) {
 __device__ __forceinline__ float tanh_accurate(float y) {
   return fabsf(y) <= 1.f ? tanh_poly13(y) : tanh_large(y);
 }
+// The same two with the derivative, for the backward pass.  1 - tanh^2 loses
+// its digits where tanh nears 1 (all of them from |y| = 9 on); with
+// E = e^(-2|y|) it is 4 E / (1 + E)^2, a product whose error stays relative.
+__device__ __forceinline__ float tanh_large(float y, float& slope) {
+  const float e = ex2(fabsf(y) * -2.8853900817779268f), r = rcp(1.f + e);
+  const float er = e * r;
+  slope = 4.f * er * r;
+  return copysignf(fmaf(-2.f, er, 1.f), y);
+}
+__device__ __forceinline__ float tanh_accurate(float y, float& slope) {
+  if (fabsf(y) > 1.f) return tanh_large(y, slope);
+  const float t = tanh_poly13(y);
+  slope = fmaf(-t, t, 1.f);
+  return t;
+}
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);

@@ -11,6 +11,62 @@ from tests.test_backward_gpu import forced, make
 pytestmark = pytest.mark.gpu
 
 
+# ---------------------------------------------------------------- softcap
+def saturated(d, low=5.0, high=9.0, cap=20.0, seed=23, b=1, h=2, lq=300, lk=300):
+    """q and k whose every |logit / cap| lies in [low, high]."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def uniform(*shape):
+        return torch.rand(shape, generator=g, device="cuda", dtype=torch.float64)
+
+    u = torch.where(uniform(1, 1, 1, d) < 0.5, -1.0, 1.0)
+    mid = math.sqrt(low * high) * cap / math.sqrt(d)      # |q| |k| of every element
+    half = math.sqrt(high / low) ** 0.5 * (1 - 2.0 ** -7)  # room for the roundings to bf16
+    size = [math.sqrt(mid) * half ** (2 * uniform(b, h, n, 1) - 1) for n in (lq, lk)]
+    q = (size[0] * u).bfloat16()
+    k = (size[1] * u * torch.where(uniform(b, h, lk, 1) < 0.5, -1.0, 1.0)).bfloat16()
+    v, do = (torch.randn(b, h, n, d, generator=g, device="cuda").bfloat16() for n in (lk, lq))
+    return q, k, v, do
+
+
+@pytest.mark.parametrize("path,d", [(0, 64), (0, 128), (1, 128), (0, 256)])
+@pytest.mark.parametrize("low,high", [(2.0, 4.0), (5.0, 7.0), (7.0, 9.0), (9.0, 11.0)])
+@pytest.mark.parametrize("sizes", [dict(), dict(h=16, lq=700, lk=800)], ids=["two terms", "one term"])
+def test_gradients_of_saturated_logits(path, d, low, high, sizes):
+    cap = 20.0
+    q, k, v, do = saturated(d, low, high, cap, **sizes)
+    kw = dict(causal=True, window=None, softcap=cap)
+    o, lse = mgq.attention_lse(q, k, v, **kw)
+    got = forced(path, lambda: mgq.attention_backward(do, q, k, v, o, lse, **kw))
+    f = ref.forward(q, k, v, **kw)
+    y = torch.where(f["see"], torch.atanh(f["t"].clamp(-1 + 1e-15, 1 - 1e-15)).abs(), torch.zeros_like(f["t"]))
+    assert low - 0.01 <= y[y > 0].min() and y.max() <= high + 0.01
+    # 1 - tanh^2 without cancellation, 4 e / (1 + e)^2 with e = e^(-2 |y|).
+    z = torch.einsum("bhqd,bhkd->bhqk", f["q"], f["k"]) * f["scale"] / cap
+    e = torch.exp(-2 * z.abs())
+    chain = 4 * e / (1 + e) ** 2
+    dod, od = do.double(), o.double()
+    p = torch.exp(f["x"] - lse.double()[..., None])
+    dp = dod @ f["v"].transpose(-1, -2)
+    delta = (dod * od).sum(-1, keepdim=True)
+    mag = dod.abs() @ f["v"].abs().transpose(-1, -2) + (dod * od).abs().sum(-1, keepdim=True)
+    ds = p * (dp - delta) * chain * f["scale"]
+    # Relative errors.  P: its logit's and lse's, as in the reference's bound.  The
+    # factor: e is off by twice the error of |y|, which is that of the product
+    # (E32 of its magnitudes) and three roundings, and by the approximate
+    # exponential, reciprocal and three products, 2^-20 together.
+    ep = ref.logit_error(f) + ref.E32 * (1 + lse.double().abs()[..., None] + cap)
+    ec = 2 * (ref.E32 * f["mag"] / cap + z.abs() * 2.0 ** -22) + 2.0 ** -20
+    err = (ref.U16 + ep + ec) * ds.abs() + f["scale"] * p * chain * ref.E32 * mag
+    g = f["group"]
+    for n, x, w, b, m in (
+            ("dq", got[0], ds @ f["k"], err @ f["k"].abs(), ds.abs() @ f["k"].abs()),
+            ("dk", got[1], ref.fold(ds.transpose(-1, -2) @ f["q"], g),
+             ref.fold(err.transpose(-1, -2) @ f["q"].abs(), g),
+             ref.fold(ds.abs().transpose(-1, -2) @ f["q"].abs(), g))):
+        ref.assert_within(n, x, w, (b + 2.0 ** -16 * m + ref.U16 * w.abs()) * (1 + ref.U16) + 1e-30)
+
+
 # ---------------------------------------------------------------- NaN and infinities
 NAN_ROWS = [
     # (batch, q_len, kv_len, hq, hkv, d, causal, window, softcap, path)
