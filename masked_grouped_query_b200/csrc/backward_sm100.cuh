@@ -145,23 +145,26 @@ __device__ __forceinline__ void bwd_store_bf16(uint32_t tm, const f2 (&v)[16]) {
   }
 }
 
+// Zeros in the columns whose bit is not set.
+__device__ __forceinline__ void bwd_hide(f2 (&pr)[16], uint32_t seen) {
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    float a, b;
+    f2_unpack(pr[c], a, b);
+    pr[c] = f2_pack(seen & (1u << (2 * c)) ? a : 0.f, seen & (2u << (2 * c)) ? b : 0.f);
+  }
+}
+
 // dS of 32 columns from what bwd_probs left (p times the factor), dP and the
-// rows' delta.  A hidden score is an exact zero whatever dP is.
+// rows' delta.  A hidden score is an exact zero whatever dP is; a visible one
+// whose p has underflowed is not: with an infinite dP it is NaN.
 __device__ __forceinline__ void bwd_ds(const f2* keep, const uint32_t (&dp)[32], const f2 (&dl)[16],
-                                       bool masked, f2 (&d)[16]) {
+                                       bool masked, uint32_t seen, f2 (&d)[16]) {
 #pragma unroll
   for (int c = 0; c < 16; ++c)
     d[c] = f2_mul(keep[c], f2_sub(f2_pack(__uint_as_float(dp[2 * c]), __uint_as_float(dp[2 * c + 1])),
                                   dl[c]));
-  if (masked) {
-#pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      float k0, k1, a, b;
-      f2_unpack(keep[c], k0, k1);
-      f2_unpack(d[c], a, b);
-      d[c] = f2_pack(k0 == 0.f ? 0.f : a, k1 == 0.f ? 0.f : b);
-    }
-  }
+  if (masked) bwd_hide(d, seen);
 }
 
 // 32 floats of shared memory, the same for every lane, as pairs.
@@ -240,16 +243,6 @@ __device__ __forceinline__ uint32_t bwd_bits(int lo, int hi) {
   hi = min(hi, 31);
   return hi < lo ? 0u : (0xffffffffu >> (31 - hi)) & (0xffffffffu << lo);
 }
-// p with the columns whose bit is not set as zeros.
-__device__ __forceinline__ void bwd_hide(f2 (&pr)[16], uint32_t seen) {
-#pragma unroll
-  for (int c = 0; c < 16; ++c) {
-    float a, b;
-    f2_unpack(pr[c], a, b);
-    pr[c] = f2_pack(seen & (1u << (2 * c)) ? a : 0.f, seen & (2u << (2 * c)) ? b : 0.f);
-  }
-}
-
 // The k-th item of this CTA: items go out in rounds of the grid, every other
 // round backwards when they are sorted heavy first, so that no CTA takes the
 // heaviest of every round.
@@ -579,6 +572,8 @@ __global__ void __launch_bounds__(kBwThreads, 1)
               if (qi >= qlo && qi <= qhi) seen[1] |= 1u << c;
               if (++qi == s.q_len) qi = 0;
             }
+            seen[0] &= bwd_bits(0, nr - 1 - 64 * h);  // rows that pad the tile see nothing
+            seen[1] &= bwd_bits(0, nr - 1 - 64 * h - 32);
           }
         }
         // P of columns 32 g .. 32 g + 31 of this half, into TMEM columns
@@ -616,10 +611,10 @@ __global__ void __launch_bounds__(kBwThreads, 1)
         tmem_ld32(dp_tm, b0);
         tmem_ld32(dp_tm + 32, b1);
         tmem_ld_wait();
-        bwd_ds(keep, b0, dl, need_mask, ds);
+        bwd_ds(keep, b0, dl, need_mask, seen[0], ds);
         bwd_store_bf16<kFine>(dp_tm, ds);
         bwd_load32(st + 160, dl);
-        bwd_ds(keep + 16, b1, dl, need_mask, ds);
+        bwd_ds(keep + 16, b1, dl, need_mask, seen[1], ds);
         bwd_store_bf16<kFine>(dp_tm + 16, ds);
         tmem_st_wait();
         tc_fence_before();
@@ -926,9 +921,9 @@ __global__ void __launch_bounds__(kBwThreads, 1)
 #pragma unroll
         for (int c = 0; c < 16; ++c) row[c] = f2_pack(delta, delta);
         tmem_ld_wait();
-        bwd_ds(keep, b0, row, need_mask, ds);
+        bwd_ds(keep, b0, row, need_mask, bwd_bits(lo - c0, hi - c0), ds);
         bwd_store_bf16<kFine>(s_tm, ds);
-        bwd_ds(keep + 16, b1, row, need_mask, ds);
+        bwd_ds(keep + 16, b1, row, need_mask, bwd_bits(lo - c0 - 32, hi - c0 - 32), ds);
         bwd_store_bf16<kFine>(s_tm + 16, ds);
         tmem_st_wait();
         tc_fence_before();

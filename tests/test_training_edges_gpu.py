@@ -125,3 +125,19 @@ def test_rows_that_are_not_numbers(case, value):
         lim = (2 * ref.U16 + 2 * lim) * (p @ v.abs()) + 1e-30
         assert ((o2[0, 1, row].double() - p @ v).abs() <= lim).all()
     assert mgq.status() & 0x1f == 0
+
+
+@pytest.mark.parametrize("path,d,lq", [(0, 64, 256), (0, 128, 256), (0, 128, 200), (1, 128, 256), (0, 256, 256)])
+@pytest.mark.parametrize("cap", [None, 50.0])
+def test_an_infinite_gradient_reaches_every_visible_key(path, d, lq, cap):
+    # Where P has underflowed to zero too (0 * inf), in tiles with a mask as in others.
+    lk = lq
+    t, kw = make((1, lq, lk, 4, 2, d, True, None, cap, 60), seed=28)
+    o, lse = mgq.attention_lse(t["q"], t["k"], t["v"], **kw)
+    row = lq - 40
+    t["do"][0, 0, row, 5] = math.inf
+    dq, dk, dv = forced(path, lambda: mgq.attention_backward(t["do"], t["q"], t["k"], t["v"], o, lse, **kw))
+    assert not torch.isfinite(dq[0, 0, row]).any()
+    assert torch.isfinite(dq[0, 0, :row]).all() and torch.isfinite(dq[0, 1:]).all()
+    assert not torch.isfinite(dk[0, 0, :row + 1]).any()
+    assert torch.isfinite(dk[0, 0, row + 1:]).all() and torch.isfinite(dk[0, 1]).all()
