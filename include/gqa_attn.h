@@ -129,7 +129,8 @@ int gqa_attn_fwd(const void* q, const void* k, const void* v, void* o, int batch
  * gqa_attn_fwd: in particular, graphs captured on one stream share that
  * stream's workspace, and replay one after the other.  The kernels behind
  * this entry point take exponentials and tanh more exactly than
- * gqa_attn_fwd's, so o may differ from its o in the last bit.
+ * gqa_attn_fwd's, so o may differ from its o in the last bit.  A softcap
+ * above 1e30 is taken as 1e30, here and in gqa_attn_bwd.
  */
 int gqa_attn_fwd_lse(const void* q, const void* k, const void* v, void* o, float* lse, int batch,
                      int q_len, int kv_len, int num_q_heads, int num_kv_heads, int head_dim,

@@ -485,7 +485,7 @@ int launch_decode_ks(const Problem& pr, const Plan& pl, DeviceInfo& dev, const v
   p.use_softcap = pr.softcap > 0.f ? 1 : 0;
   const float rs = 1.0f / std::sqrt((float)pr.d);
   p.logit_scale = kLog2e * rs;
-  p.cap_in = p.use_softcap ? rs / pr.softcap : 0.f;
+  p.cap_in = p.use_softcap ? gqa_host::softcap_in(rs, pr.softcap) : 0.f;
   p.cap_out = p.use_softcap ? pr.softcap * kLog2e : 0.f;
   p.splits = pl.splits;
   p.tiles_per_split = pl.tps;
@@ -680,7 +680,7 @@ int launch_prefill_k(const Problem& pr, const Plan& pl, DeviceInfo& dev, int csi
   p.window = pr.window;
   const float rs = 1.0f / std::sqrt((float)pr.d);
   p.logit_scale = kLog2e * rs;
-  p.cap_in = kCap ? rs / pr.softcap : 0.f;
+  p.cap_in = kCap ? gqa_host::softcap_in(rs, pr.softcap) : 0.f;
   p.cap_out = kCap ? pr.softcap * kLog2e : 0.f;
   // Fixed exponent base (softcap code 3, see PrefillParams and cap_degree).
   p.cap_fixed = kCapDeg == 3 ? 1 : 0;
@@ -932,6 +932,7 @@ int gqa_attn_fwd_lse(const void* q, const void* k, const void* v, void* o, float
     return GQA_ATTN_ERR_ALIAS;
   if (rows == 0) return GQA_ATTN_OK;
   pr.lse = lse;
+  pr.softcap = std::min(pr.softcap, gqa_host::kSoftcapMost);
   return run(pr, q, k, v, o, (cudaStream_t)stream);
 }
 

@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -346,10 +347,11 @@ int gqa_attn_bwd(const void* dout, const void* q, const void* k, const void* v, 
   p.part_dk = (float*)((char*)scratch + pl.off_dk);
   p.part_dv = (float*)((char*)scratch + pl.off_dv);
   p.part_dq = (float*)((char*)scratch + pl.off_dq);
+  softcap = std::min(softcap, gqa_host::kSoftcapMost);
   p.softcap = softcap > 0.f;
   p.scale = 1.0f / std::sqrt((float)head_dim);
   p.logit_scale = kLog2e32 * p.scale;
-  p.cap_in = p.softcap ? p.scale / softcap : 0.f;
+  p.cap_in = p.softcap ? gqa_host::softcap_in(p.scale, softcap) : 0.f;
   p.cap_out = p.softcap ? softcap * kLog2e32 : 0.f;
   bwd_stats_kernel<<<(unsigned)(s.runs * s.tiles), kBwStatThreads, 0, st>>>(
       p.dout, (const __nv_bfloat16*)o, lse, dlse, (float*)scratch, s);

@@ -2,6 +2,10 @@
 // translation unit.
 #pragma once
 
+#include <cfloat>
+
+#include <algorithm>
+
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
@@ -25,6 +29,13 @@ int forced_path();
 int cuda_fail(const char* where, cudaError_t e, int code);
 // The same for a message of this library.
 int detail(int code, const char* fmt, ...);
+
+// The training operators take softcaps above this one as this one: neither
+// changes a logit up to 1e26 in fp32 (by (x / cap)^2 / 3 of itself), and with
+// this one the scales derived from it stay normal numbers.
+constexpr float kSoftcapMost = 1e30f;
+// 1 / (sqrt(head_dim) * softcap), finite for every softcap.
+inline float softcap_in(float scale, float softcap) { return std::min(scale / softcap, FLT_MAX); }
 
 bool overlaps(const void* a, size_t na, const void* b, size_t nb);
 

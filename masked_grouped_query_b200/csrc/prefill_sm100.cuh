@@ -696,6 +696,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll
       for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(ov[e]);
     };
+    // Largest |x * cap_in| that takes tanh's polynomial.
+    const float poly_most = !kLse ? 0.5f : p.cap_in <= kFoldMaxCapIn ? 1.f : -1.f;
     int n_s = 0;      // S tiles consumed (s_full[t] phases)
     int n_busy = 0;   // busy items finished (o_done phases)
     int n_merge = 0;  // split tickets taken by this warpgroup (part_done[t] phases)
@@ -752,7 +754,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll
               for (int c = 2; c < 32; c += 2)
                 am = fmax3(am, fabsf(__uint_as_float(sv[c])), fabsf(__uint_as_float(sv[c + 1])));
-              const bool poly = __all_sync(0xffffffffu, am * p.cap_in <= (kLse ? 1.f : 0.5f));
+              const bool poly = __all_sync(0xffffffffu, am * p.cap_in <= poly_most);
               if (need_mask) {
 #pragma unroll
                 for (int c = 0; c < 32; ++c)
@@ -873,7 +875,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             mraw = fmax3(mraw, m2[0], m2[1]);
           }
           if (need_mask) tmem_st_wait();  // pass 2 reads the masked scores
-          if constexpr (kCap) small_y = __all_sync(0xffffffffu, amax * p.cap_in <= (kLse ? 1.f : 0.5f));
+          if constexpr (kCap) small_y = __all_sync(0xffffffffu, amax * p.cap_in <= poly_most);
         }
         const float mt = mraw == -INFINITY ? -INFINITY
                          : kCap ? p.cap_out * tanh_fast(mraw * p.cap_in)

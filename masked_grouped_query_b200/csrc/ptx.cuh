@@ -447,6 +447,9 @@ constexpr float kTanh13C7 = -0.05349045619368553f;
 constexpr float kTanh13C9 = 0.0202915258705616f;
 constexpr float kTanh13C11 = -0.006167485378682613f;
 constexpr float kTanh13C13 = 0.0010202169651165605f;
+// Kernels that fold cap_in's powers into a polynomial's coefficients take it
+// for cap_in up to this: past it (softcaps below 1e-3) the powers overflow.
+constexpr float kFoldMaxCapIn = 1e3f;
 __device__ __forceinline__ float tanh_poly13(float y) {
   const float y2 = y * y;
   float q = fmaf(kTanh13C13, y2, kTanh13C11);

@@ -67,6 +67,43 @@ def test_gradients_of_saturated_logits(path, d, low, high, sizes):
         ref.assert_within(n, x, w, (b + 2.0 ** -16 * m + ref.U16 * w.abs()) * (1 + ref.U16) + 1e-30)
 
 
+@pytest.mark.parametrize("path,d", [(0, 64), (1, 128), (0, 128), (0, 256)])
+@pytest.mark.parametrize("cap", [1e-5, 1e-39, 3e38])
+@pytest.mark.parametrize("sizes", [(1, 200, 300, 4, 2), (4, 700, 700, 16, 16), (2, 1, 300, 4, 2)], ids=str)
+def test_softcaps_at_the_ends_of_their_range(path, d, cap, sizes):
+    b, lq, lk, hq, hkv = sizes
+    t, kw = make((b, lq, lk, hq, hkv, d, True, None, cap, 1), seed=24)
+    t["q"][:, ::2] = 0  # logits of exactly zero
+    f = ref.forward(t["q"], t["k"], t["v"], **{**kw, "softcap": cap if cap < 1 else None})
+    o, lse = forced(path, lambda: mgq.attention_lse(t["q"], t["k"], t["v"], **kw))
+    plain = {**f, "softcap": 0.0 if cap > 1 else cap}
+    ref.assert_within("o", o, f["o"], ref.o_bound(plain))
+    ref.assert_within("lse", lse, f["lse"], ref.lse_bound(plain))
+    got = forced(path, lambda: mgq.attention_backward(t["do"], t["q"], t["k"], t["v"], o, lse, **kw))
+    want, bound = ref.backward(t["q"], t["k"], t["v"], o, lse, t["do"], None, True, None,
+                               cap if cap < 1 else None)
+    bound = list(bound)
+    if cap < 1:
+        # The slope sech^2(y), y = x / cap, also moves with the error of the fp32
+        # product x (E32 of its magnitudes): between sech^2(|y| + dy) and
+        # sech^2(|y| - dy), which for these caps is all of it near x = 0.
+        z = torch.einsum("bhqd,bhkd->bhqk", f["q"], f["k"]).abs() * f["scale"]
+        dz = ref.E32 * f["mag"]
+
+        def slope(x):
+            e = torch.exp(-2 * (x / cap).clamp(max=300))
+            return 4 * e / (1 + e) ** 2
+
+        do, od = t["do"].double(), o.double()
+        p = torch.exp(f["x"] - lse.double()[..., None])
+        dp = do @ f["v"].transpose(-1, -2) - (do * od).sum(-1, keepdim=True)
+        room = p * dp.abs() * (slope((z - dz).clamp(min=0)) - slope(z + dz)) * f["scale"] * (1 + 2 * ref.U16)
+        bound[0] = bound[0] + room @ f["k"].abs()
+        bound[1] = bound[1] + ref.fold(room.transpose(-1, -2) @ f["q"].abs(), f["group"])
+    for n, x, w, r in zip(("dq", "dk", "dv"), got, want, bound):
+        ref.assert_within(n, x, w, r)
+
+
 # ---------------------------------------------------------------- NaN and infinities
 NAN_ROWS = [
     # (batch, q_len, kv_len, hq, hkv, d, causal, window, softcap, path)
