@@ -129,16 +129,21 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 }
 
 // cap_out * tanh(x * cap_in) + c for a pair with |x * cap_in| <= 1, as x Q(x^2)
-// with the scales folded into the degree-13 polynomial's coefficients.
+// with the scales folded into the degree-13 polynomial's coefficients.  kFold
+// also folds cap_in's powers, for softcaps up to 64 only: past 150 the top ones
+// underflow (an error of 0.3 in a logit of 300 below a cap of 300).
+template <bool kFold>
 struct LogitPoly13 {
-  f2 q[7];
+  f2 q[7], in;
   __device__ __forceinline__ LogitPoly13(float cap_in, float cap_out) {
+    in = f2_pack(cap_in, cap_in);
     const float k[7] = {kTanh13C1, kTanh13C3, kTanh13C5, kTanh13C7, kTanh13C9, kTanh13C11, kTanh13C13};
-    float f = cap_in * cap_out;
+    float f = kFold ? cap_in * cap_out : cap_out;
 #pragma unroll
-    for (int i = 0; i < 7; ++i, f *= cap_in * cap_in) q[i] = f2_pack(f * k[i], f * k[i]);
+    for (int i = 0; i < 7; ++i, f *= kFold ? cap_in * cap_in : 1.f) q[i] = f2_pack(f * k[i], f * k[i]);
   }
   __device__ __forceinline__ f2 operator()(f2 x, f2 c) const {
+    if constexpr (!kFold) x = f2_mul(x, in);
     const f2 x2 = f2_mul(x, x);
     f2 r = q[6];
 #pragma unroll
@@ -747,7 +752,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             const f2 q0 = f2_pack(cc * kTanh5C1, cc * kTanh5C1);
             const f2 q1 = f2_pack(cc * ci2 * kTanh5C3, cc * ci2 * kTanh5C3);
             const f2 q2 = f2_pack(cc * ci2 * ci2 * kTanh5C5, cc * ci2 * ci2 * kTanh5C5);
-            const LogitPoly13 logit13(p.cap_in, p.cap_out);  // kLse only
+            const LogitPoly13<true> logit13(p.cap_in, p.cap_out);  // kLse only
             f2 acc[4] = {0ull, 0ull, 0ull, 0ull};
             auto group = [&](uint32_t(&sv)[32], int g) {
               float am = fmaxf(fabsf(__uint_as_float(sv[0])), fabsf(__uint_as_float(sv[1])));
@@ -971,7 +976,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               return f2_fma(v, f2_fma(f2_fma(q2, v2, q1), v2, q0), nb);
             }, No());
           } else if constexpr (kLse) {
-            const LogitPoly13 poly(p.cap_in, p.cap_out);
+            const LogitPoly13<false> poly(p.cap_in, p.cap_out);
             emit([&](f2 v) { return poly(v, nb); }, Yes());
           } else {
             const f2 q0 = f2_pack(cc * kTanhC1, cc * kTanhC1);

@@ -450,6 +450,8 @@ constexpr float kTanh13C13 = 0.0010202169651165605f;
 // Kernels that fold cap_in's powers into a polynomial's coefficients take it
 // for cap_in up to this: past it (softcaps below 1e-3) the powers overflow.
 constexpr float kFoldMaxCapIn = 1e3f;
+// The degree-7 fit's top power, the seventh, stays a normal number down to this.
+constexpr float kFoldMinCapIn = 1e-5f;
 __device__ __forceinline__ float tanh_poly13(float y) {
   const float y2 = y * y;
   float q = fmaf(kTanh13C13, y2, kTanh13C11);

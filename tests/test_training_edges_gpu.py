@@ -11,6 +11,24 @@ from tests.test_backward_gpu import forced, make
 pytestmark = pytest.mark.gpu
 
 
+# ---------------------------------------------------------------- statistics with large softcaps
+def check_forward_and_gradients(case, kw, t, path):
+    f = ref.forward(t["q"], t["k"], t["v"], **kw)
+    o, lse = forced(path, lambda: mgq.attention_lse(t["q"], t["k"], t["v"], **kw))
+    ref.assert_within("o", o, f["o"], ref.o_bound(f))
+    empty = f["lse"] == -math.inf
+    assert torch.equal(lse == -math.inf, empty)
+    assert (o[empty] == 0).all()
+    zero = torch.zeros_like(f["lse"])
+    ref.assert_within("lse", torch.where(empty, zero, lse.double()), torch.where(empty, zero, f["lse"]),
+                      ref.lse_bound(f))
+    want, bound = ref.backward(t["q"], t["k"], t["v"], o, lse, t["do"], None, **kw)
+    got = forced(path, lambda: mgq.attention_backward(t["do"], t["q"], t["k"], t["v"], o, lse, **kw))
+    for n, g, w, b in zip(("dq", "dk", "dv"), got, want, bound):
+        ref.assert_within(n, g, w, b)
+    assert mgq.status() & 0x1f == 0
+
+
 # ---------------------------------------------------------------- softcap
 def saturated(d, low=5.0, high=9.0, cap=20.0, seed=23, b=1, h=2, lq=300, lk=300):
     """q and k whose every |logit / cap| lies in [low, high]."""
@@ -65,6 +83,17 @@ def test_gradients_of_saturated_logits(path, d, low, high, sizes):
              ref.fold(err.transpose(-1, -2) @ f["q"].abs(), g),
              ref.fold(ds.abs().transpose(-1, -2) @ f["q"].abs(), g))):
         ref.assert_within(n, x, w, (b + 2.0 ** -16 * m + ref.U16 * w.abs()) * (1 + ref.U16) + 1e-30)
+
+
+@pytest.mark.parametrize("path,d", [(0, 64), (0, 128), (1, 64), (0, 256)])
+@pytest.mark.parametrize("cap", [60.0, 80.0, 150.0, 300.0, 1000.0, 1e4, 1e5])
+@pytest.mark.parametrize("high", [0.48, 0.96])
+@pytest.mark.parametrize("sizes", [dict(), dict(h=16, lq=700, lk=800)], ids=["small", "large"])
+def test_logits_below_large_softcaps(path, d, cap, high, sizes):
+    # |logit / cap| up to 1/2 and up to 1, the polynomials' ranges.
+    q, k, v, do = saturated(d, 0.25, high, cap, seed=30, **sizes)
+    check_forward_and_gradients(None, dict(causal=True, window=None, softcap=cap), dict(q=q, k=k, v=v, do=do),
+                                path)
 
 
 @pytest.mark.parametrize("path,d", [(0, 64), (1, 128), (0, 128), (0, 256)])
