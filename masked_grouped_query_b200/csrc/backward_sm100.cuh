@@ -99,22 +99,9 @@ __device__ __forceinline__ void bwd_probs(const BwdParams& p, const uint32_t (&s
 #pragma unroll
     for (int c = 0; c < 32; c += 2)
       am = fmax3(am, fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
-    const bool small = __all_sync(0xffffffffu, am * p.cap_in <= 0.5f) && p.cap_in <= kFoldMaxCapIn;
+    const bool small = __all_sync(0xffffffffu, am * p.cap_in <= 0.5f);
     const f2 co = f2_pack(p.cap_out, p.cap_out), one = f2_pack(1.f, 1.f);
-    if (small && p.cap_in < kFoldMinCapIn) {
-      // Huge softcaps: cap_in's powers would underflow, so x is scaled first.
-      const f2 ci = f2_pack(p.cap_in, p.cap_in);
-      const f2 c1 = f2_pack(kTanhC1, kTanhC1), c3 = f2_pack(kTanhC3, kTanhC3);
-      const f2 c5 = f2_pack(kTanhC5, kTanhC5), c7 = f2_pack(kTanhC7, kTanhC7);
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const f2 x = f2_mul(f2_pack(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), ci);
-        const f2 x2 = f2_mul(x, x);
-        const f2 t = f2_mul(x, f2_fma(f2_fma(f2_fma(c7, x2, c5), x2, c3), x2, c1));
-        pr[c] = exp2_mufu_x2(f2_fma(co, t, nl[c]));
-        fac[c] = f2_fma(t, t ^ 0x8000000080000000ull, one);
-      }
-    } else if (small) {
+    if (small) {
       // tanh(x cap_in) as x Q(x^2), cap_in folded into the coefficients.
       const float i2 = p.cap_in * p.cap_in;
       const float q1 = kTanhC1 * p.cap_in, q3 = kTanhC3 * p.cap_in * i2;
@@ -129,13 +116,18 @@ __device__ __forceinline__ void bwd_probs(const BwdParams& p, const uint32_t (&s
         fac[c] = f2_fma(t, t ^ 0x8000000080000000ull, one);
       }
     } else {
+      // Two of tanh_large at a time.
+      const float in = p.cap_in * 2.8853900817779268f;
+      const f2 half = f2_pack(0.5f, 0.5f), ci = f2_pack(in, in);
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
-        float fa, fb;
-        const float a = tanh_large(__uint_as_float(s[2 * c]) * p.cap_in, fa);
-        const float b = tanh_large(__uint_as_float(s[2 * c + 1]) * p.cap_in, fb);
-        pr[c] = exp2_mufu_x2(f2_fma(co, f2_pack(a, b), nl[c]));
-        fac[c] = f2_pack(fa, fb);
+        float a, b;
+        f2_unpack(f2_mul(f2_pack(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), ci), a, b);
+        const f2 u = exp2_mufu_x2(f2_pack(min_nan(a, 100.f), min_nan(b, 100.f)));
+        f2_unpack(f2_fma(u, half, half), a, b);
+        const f2 h = f2_pack(rcp(a), rcp(b));
+        pr[c] = exp2_mufu_x2(f2_fma(co, f2_sub(one, h), nl[c]));
+        fac[c] = f2_mul(f2_mul(u, h), h);
       }
     }
   }

@@ -306,8 +306,15 @@ int gqa_attn_bwd(const void* dout, const void* q, const void* k, const void* v, 
        (uintptr_t)scratch) & 15u)
     return GQA_ATTN_ERR_MISALIGNED;
   const bool work = q_bytes && kv_bytes;
-  // (force_path 1 takes the mma.sync kernels for narrow heads too, uncut.)
-  const bool narrow_mma = head_dim <= 128 && gqa_host::forced_path() == 1;
+  softcap = std::min(softcap, gqa_host::kSoftcapMost);
+  p.softcap = softcap > 0.f;
+  p.scale = 1.0f / std::sqrt((float)head_dim);
+  p.cap_in = p.softcap ? gqa_host::softcap_in(p.scale, softcap) : 0.f;
+  // Narrow heads take the mma.sync kernels too (uncut) when asked by
+  // force_path 1, and with softcaps for which the tcgen05 kernels cannot fold
+  // the powers of cap_in into their polynomial.
+  const bool folds = !p.softcap || (p.cap_in >= kFoldMinCapIn && p.cap_in <= kFoldMaxCapIn);
+  const bool narrow_mma = head_dim <= 128 && (gqa_host::forced_path() == 1 || !folds);
   const BwdPlan pl = bwd_plan(s, !narrow_mma);
   const size_t need = work ? pl.bytes : 0;
   if (need && !scratch) return GQA_ATTN_ERR_NULL_POINTER;
@@ -347,11 +354,7 @@ int gqa_attn_bwd(const void* dout, const void* q, const void* k, const void* v, 
   p.part_dk = (float*)((char*)scratch + pl.off_dk);
   p.part_dv = (float*)((char*)scratch + pl.off_dv);
   p.part_dq = (float*)((char*)scratch + pl.off_dq);
-  softcap = std::min(softcap, gqa_host::kSoftcapMost);
-  p.softcap = softcap > 0.f;
-  p.scale = 1.0f / std::sqrt((float)head_dim);
   p.logit_scale = kLog2e32 * p.scale;
-  p.cap_in = p.softcap ? gqa_host::softcap_in(p.scale, softcap) : 0.f;
   p.cap_out = p.softcap ? softcap * kLog2e32 : 0.f;
   bwd_stats_kernel<<<(unsigned)(s.runs * s.tiles), kBwStatThreads, 0, st>>>(
       p.dout, (const __nv_bfloat16*)o, lse, dlse, (float*)scratch, s);

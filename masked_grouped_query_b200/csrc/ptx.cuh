@@ -447,10 +447,11 @@ constexpr float kTanh13C7 = -0.05349045619368553f;
 constexpr float kTanh13C9 = 0.0202915258705616f;
 constexpr float kTanh13C11 = -0.006167485378682613f;
 constexpr float kTanh13C13 = 0.0010202169651165605f;
-// Kernels that fold cap_in's powers into a polynomial's coefficients take it
-// for cap_in up to this: past it (softcaps below 1e-3) the powers overflow.
+// Folding cap_in's powers into a polynomial's coefficients saves one product
+// per pair of scores and works between these: past the first (softcaps below
+// 1e-3) the 13th power overflows, below the second (softcaps past 10^4) the 7th,
+// of the backward pass, is no normal number.
 constexpr float kFoldMaxCapIn = 1e3f;
-// The degree-7 fit's top power, the seventh, stays a normal number down to this.
 constexpr float kFoldMinCapIn = 1e-5f;
 __device__ __forceinline__ float tanh_poly13(float y) {
   const float y2 = y * y;
@@ -471,13 +472,19 @@ __device__ __forceinline__ float tanh_accurate(float y) {
   return fabsf(y) <= 1.f ? tanh_poly13(y) : tanh_large(y);
 }
 // The same two with the derivative, for the backward pass.  1 - tanh^2 loses
-// its digits where tanh nears 1 (all of them from |y| = 9 on); with
-// E = e^(-2|y|) it is 4 E / (1 + E)^2, a product whose error stays relative.
+// its digits where tanh nears 1 (all of them from |y| = 9 on); with u = e^2y
+// and h = 2 / (1 + u) it is u h^2, a product whose error stays relative, and
+// tanh is 1 - h.  u stops at 2^100, so that u h does not overflow (NaN goes on).
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
 __device__ __forceinline__ float tanh_large(float y, float& slope) {
-  const float e = ex2(fabsf(y) * -2.8853900817779268f), r = rcp(1.f + e);
-  const float er = e * r;
-  slope = 4.f * er * r;
-  return copysignf(fmaf(-2.f, er, 1.f), y);
+  const float u = ex2(min_nan(y * 2.8853900817779268f, 100.f));
+  const float h = rcp(fmaf(u, 0.5f, 0.5f));
+  slope = u * h * h;
+  return 1.f - h;
 }
 __device__ __forceinline__ float tanh_accurate(float y, float& slope) {
   if (fabsf(y) > 1.f) return tanh_large(y, slope);
