@@ -882,8 +882,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           if (need_mask) tmem_st_wait();  // pass 2 reads the masked scores
           if constexpr (kCap) small_y = __all_sync(0xffffffffu, amax * p.cap_in <= poly_most);
         }
+        // With statistics wanted the base's tanh is the scores' own: the
+        // hardware's error, times a softcap of 10^8, is more than the exponents
+        // of p span.
         const float mt = mraw == -INFINITY ? -INFINITY
-                         : kCap ? p.cap_out * tanh_fast(mraw * p.cap_in)
+                         : kCap ? p.cap_out * (!kLse     ? tanh_fast(mraw * p.cap_in)
+                                               : small_y ? tanh_poly13(mraw * p.cap_in)
+                                                         : tanh_large(mraw * p.cap_in))
                                 : mraw * p.logit_scale;
         // Rescale only when the max grew by more than 2^8 (or was -inf): the
         // stale max keeps p <= 256, and O / l stays consistent.

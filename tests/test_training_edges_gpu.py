@@ -133,6 +133,20 @@ def test_softcaps_at_the_ends_of_their_range(path, d, cap, sizes):
         ref.assert_within(n, x, w, r)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap", [1e6, 1e7, 1e8])
+@pytest.mark.parametrize("sizes", [(1, 200, 300, 4, 2), (4, 700, 700, 16, 16)], ids=str)
+def test_running_maximum_of_huge_logits(d, cap, sizes):
+    # Logits of about a third of such caps: a maximum that is off by the hardware
+    # tanh's error, times the cap, is off by more than fp32's exponents span.
+    t, kw = make((*sizes, d, True, None, cap, 1), seed=25)
+    t["q"] = (t["q"].float() * 0.3 * cap).bfloat16()
+    f = ref.forward(t["q"], t["k"], t["v"], **kw)
+    o, lse = mgq.attention_lse(t["q"], t["k"], t["v"], **kw)
+    assert torch.isfinite(o).all()
+    ref.assert_within("lse", lse, f["lse"], ref.lse_bound(f))
+
+
 # ---------------------------------------------------------------- NaN and infinities
 NAN_ROWS = [
     # (batch, q_len, kv_len, hq, hkv, d, causal, window, softcap, path)
