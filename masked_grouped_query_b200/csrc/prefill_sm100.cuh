@@ -885,7 +885,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         // With statistics wanted the base's tanh is the scores' own: the
         // hardware's error, times a softcap of 10^8, is more than the exponents
         // of p span.
-        const float mt = mraw == -INFINITY ? -INFINITY
+        // A visible score of -inf is -softcap there.
+        const bool some = mraw != -INFINITY || (kLse && kCap && vlo < kPfN);
+        const float mt = !some ? -INFINITY
                          : kCap ? p.cap_out * (!kLse     ? tanh_fast(mraw * p.cap_in)
                                                : small_y ? tanh_poly13(mraw * p.cap_in)
                                                          : tanh_large(mraw * p.cap_in))

@@ -207,6 +207,22 @@ def test_rows_that_are_not_numbers(case, value):
     assert mgq.status() & 0x1f == 0
 
 
+@pytest.mark.parametrize("case", [c for c in NAN_ROWS if c[8]], ids=str)
+def test_a_row_of_minus_infinities_below_the_cap(case):
+    # Every visible logit is -inf, which the cap makes -cap: the plain mean of v.
+    case, path = dims(case)
+    t, kw = make(case, seed=27)
+    row = case[1] // 2
+    t["k"][..., 3] = -t["k"][..., 3].abs() - 0.01
+    t["q"][0, 0, row, 3] = math.inf
+    o, lse = forced(path, lambda: mgq.attention_lse(t["q"], t["k"], t["v"], **kw))
+    see = ref.visible(case[1], case[2], case[6], case[7], "cuda")[row]
+    want = math.log(see.sum().item()) - kw["softcap"]
+    assert abs(lse[0, 0, row].item() - want) <= kw["softcap"] * 4e-7 + ref.E32 * (1 + abs(want) + kw["softcap"])
+    v = t["v"][0, 0].double()[see]
+    assert ((o[0, 0, row].double() - v.mean(0)).abs() <= 2 * ref.U16 * v.abs().mean(0) + 1e-30).all()
+
+
 @pytest.mark.parametrize("path,d,lq", [(0, 64, 256), (0, 128, 256), (0, 128, 200), (1, 128, 256), (0, 256, 256)])
 @pytest.mark.parametrize("cap", [None, 50.0])
 def test_an_infinite_gradient_reaches_every_visible_key(path, d, lq, cap):
