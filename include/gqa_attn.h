@@ -197,8 +197,9 @@ int gqa_attn_bwd_scratch(int batch, int q_len, int kv_len, int num_q_heads, int 
  * to axis 1, and so on.  Pair i, the j-th of its axis a, of token l of batch
  * row b turns by positions[a][b][l] * f with f = theta^(-i / pairs), or
  * theta^(-j / sections[a]) with GQA_ROTARY_PER_AXIS.  Elements past the last
- * pair are copied.  Angles are exact to 1e-6 for positions of 32 bits, the
- * rotation is fp32, rounded once.
+ * pair are copied.  An angle a = position * f is good to 2^-51 |a| + 3e-7, which
+ * for positions of 32 bits and theta >= 1 is below 1e-6; the rotation is fp32,
+ * rounded once.
  *
  * q, q_out have num_q_heads heads, k, k_out num_kv_heads; either count may be
  * 0 (its pointers are then ignored), not both.  positions is

@@ -451,19 +451,21 @@ int gqa_attn_rotary(const void* q, const void* k, void* q_out, void* k_out, cons
     p.out_l[w] = out_seq ? h * d : d;
   }
   // Frequency of pair i: theta^(-i / pairs), or theta^(-j / section) for the
-  // j-th pair of its axis, as turns per position.
-  // One power a step: the products' rounding grows by 2^-53 a pair.
-  const double pi2 = 6.283185307179586476925286766559;
+  // j-th pair of its axis, as turns per position.  A running product in the
+  // wider type: ratio's own rounding enters every power, 128 of them lose seven
+  // bits, of which fp64 has none to spare at positions of 2^31.  128 pairs take
+  // a host core 0.6 us so; 1.7 with a power for each, 0.2 in fp64.
+  const long double pi2 = 6.283185307179586476925286766559L;
   const bool per_axis = flags & GQA_ROTARY_PER_AXIS;
-  double ratio = std::pow(theta, -1.0 / (double)pairs), f = 1.0;
+  long double ratio = std::pow((long double)theta, -1.0L / pairs), f = 1.0L;
   int at = 0;
   for (int a = 0; a < num_axes; ++a) {
     if (per_axis) {
-      ratio = std::pow(theta, -1.0 / sections[a]);
-      f = 1.0;
+      ratio = std::pow((long double)theta, -1.0L / sections[a]);
+      f = 1.0L;
     }
     for (int j = 0; j < sections[a]; ++j, ++at, f *= ratio) {
-      p.turn[at] = f / pi2;
+      p.turn[at] = (double)(f / pi2);
       p.axis[at] = (unsigned char)a;
     }
   }

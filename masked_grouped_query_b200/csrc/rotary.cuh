@@ -6,10 +6,10 @@
 // also the gradient (the rotation is orthogonal).  Elements past the last
 // pair pass through.
 //
-// The angle is kept in turns: position * (f / 2 pi) in fp64, whose fraction
-// is exact to 2^-20 of a turn or better for every 32-bit position (an fp32
-// product would lose the fraction at positions of some thousands), then
-// sincospi of the fp32 fraction.
+// The angle is kept in turns: position * (f / 2 pi) in fp64, two roundings of
+// 2^-53 relative, then sincospi of the fraction in fp32 (2^-25 of a turn).  For
+// 32-bit positions and frequencies up to 1 that is 7e-7 radians (an fp32
+// product would lose the fraction at positions of some thousands).
 //
 // Bound by memory: q and k are read and written once.  A thread computes the
 // sine and cosine of V pairs of one token once and applies them to a run of

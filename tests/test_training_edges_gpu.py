@@ -1,5 +1,6 @@
 """The training operators where their formulas are easy to get wrong (GPU)."""
 import math
+from decimal import Decimal, getcontext
 
 import pytest
 import torch
@@ -27,6 +28,42 @@ def check_forward_and_gradients(case, kw, t, path):
     for n, g, w, b in zip(("dq", "dk", "dv"), got, want, bound):
         ref.assert_within(n, g, w, b)
     assert mgq.status() & 0x1f == 0
+
+
+# ---------------------------------------------------------------- rotary
+def exact_turns(sections, theta, per_axis, positions):
+    """Angles in turns, reduced to [0, 1): 96 bits of every frequency, whole-number products."""
+    getcontext().prec = 60
+    pi2, ln = Decimal("6.28318530717958647692528676655900576839433879875021164"), Decimal(theta).ln()
+    out, i = [], 0
+    for a, s in enumerate(sections):
+        for j in range(s):
+            f = (-ln * j / s if per_axis else -ln * i / sum(sections)).exp() / pi2
+            f = int((f * 2 ** 96).to_integral_value())
+            i += 1
+            out.append([(p * f % 2 ** 96) / 2 ** 96 for p in positions[a]])
+    return torch.tensor(out, dtype=torch.float64, device="cuda").T  # (length, pairs)
+
+
+@pytest.mark.parametrize("theta", [0.01, 0.5, 1.0, 1.01, 1.5, 10.0, 100.0])
+@pytest.mark.parametrize("sections,per_axis", [((32,), False), ((128,), False), ((61, 64), True)])
+def test_rotary_frequencies_of_slow_decay(theta, sections, per_axis):
+    # Positions near 2^31, where the frequencies stay near one.  Every angle is
+    # good to 1e-6 (times 1 / theta below theta 1); the sine, the cosine and the
+    # fp32 products add a few 2^-24 (4e-7) of the pair's magnitudes.
+    g = torch.Generator(device="cuda").manual_seed(22)
+    n, pairs = 1000, sum(sections)
+    q = torch.randn(1, 1, n, 256, generator=g, device="cuda")
+    pos = torch.randint((1 << 31) - 100000, 1 << 31, (len(sections), 1, n), generator=g, device="cuda")
+    pos[:, :, ::3] *= -1
+    got, _ = mgq.rotary(q, None, pos, sections=sections, theta=theta, per_axis=per_axis)
+    angle = exact_turns(sections, theta, per_axis, pos[:, 0].tolist()) * (2 * math.pi)
+    x, z = (q[0, 0, :, i:i + pairs].double() for i in (0, pairs))
+    want = torch.cat([x * angle.cos() - z * angle.sin(), z * angle.cos() + x * angle.sin()], -1)
+    mag = (x.abs() + z.abs()).repeat(1, 2)
+    lim = (1e-6 * max(1.0, 1.0 / theta) + 4e-7) * mag + 2.0 ** -24 * want.abs()
+    over = (got[0, 0, :, :2 * pairs].double() - want).abs() / lim
+    assert over.max().item() <= 1.0, over.max().item()
 
 
 # ---------------------------------------------------------------- softcap
