@@ -409,8 +409,10 @@ int gqa_attn_rotary(const void* q, const void* k, void* q_out, void* k_out, cons
   const void* in[2] = {q, k};
   void* out[2] = {q_out, k_out};
   if (tokens && !positions) return GQA_ATTN_ERR_NULL_POINTER;
-  if (((uintptr_t)positions | (uintptr_t)q | (uintptr_t)k | (uintptr_t)q_out | (uintptr_t)k_out) & 15u)
-    return GQA_ATTN_ERR_MISALIGNED;
+  uintptr_t bits = (uintptr_t)positions;
+  if (num_q_heads) bits |= (uintptr_t)q | (uintptr_t)q_out;
+  if (num_kv_heads) bits |= (uintptr_t)k | (uintptr_t)k_out;
+  if (bits & 15u) return GQA_ATTN_ERR_MISALIGNED;
   const size_t ie = in32 ? 4 : 2, oe = out32 ? 4 : 2;
   const size_t pos_bytes = (size_t)num_axes * (size_t)tokens * ((flags & GQA_ROTARY_POS_I64) ? 8 : 4);
   for (int w = 0; w < 2; ++w) {

@@ -1,0 +1,24 @@
+"""Argument checks of the training operators and the build, without a device (CPU)."""
+import pytest
+import torch
+
+from masked_grouped_query_b200 import _lib, build
+from tests.test_training_boundary import A, _rot
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return _lib.load()
+
+
+def test_rotary_ignores_the_pointers_of_no_heads(lib):
+    # Whatever they are: misaligned, or over another tensor.
+    for bad in (A[1] + 8, A[0] + 4, 3):
+        assert _rot(lib, {1: bad, 3: bad}, hkv=0, length=0) == 0
+        assert _rot(lib, {0: bad, 2: bad}, hq=0, length=0) == 0
+    assert _rot(lib, {0: A[0] + 8}, hkv=0) == -2
+    assert _rot(lib, {3: A[3] + 8}, hq=0) == -2
+    if not torch.cuda.is_available():  # past the checks, to the device's
+        assert _rot(lib, {1: A[1] + 8, 3: A[0]}, hkv=0) == -7
+        assert _rot(lib, {0: A[0] + 8, 2: A[1]}, hq=0) == -7
