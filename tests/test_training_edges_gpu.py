@@ -66,6 +66,14 @@ def test_rotary_frequencies_of_slow_decay(theta, sections, per_axis):
     assert over.max().item() <= 1.0, over.max().item()
 
 
+def test_rotary_sections_that_no_int_holds():
+    q = torch.zeros(1, 2, 3, 128, device="cuda")
+    pos = torch.zeros(1, 1, 3, dtype=torch.int32, device="cuda")
+    for sections in ((2 ** 32 + 32,), (2 ** 33,), (-2 ** 32 + 32,), (32.5,)):
+        with pytest.raises(ValueError, match="whole numbers"):
+            mgq.rotary(q, None, pos, sections=sections)
+
+
 # ---------------------------------------------------------------- softcap
 def saturated(d, low=5.0, high=9.0, cap=20.0, seed=23, b=1, h=2, lq=300, lk=300):
     """q and k whose every |logit / cap| lies in [low, high]."""
