@@ -35,7 +35,8 @@ def _check_tensor(name, t, ndim=4):
 
 
 def _args(window, softcap, causal):
-    w = 0 if window is None else int(window)
+    # A C int: past it a window would be taken modulo 2^32, as none or a short one.
+    w = 0 if window is None else max(-2 ** 31, min(int(window), 2 ** 31 - 1))
     s = 0.0 if softcap is None else float(softcap)
     return int(bool(causal)), w, s
 

@@ -22,3 +22,9 @@ def test_rotary_ignores_the_pointers_of_no_heads(lib):
     if not torch.cuda.is_available():  # past the checks, to the device's
         assert _rot(lib, {1: A[1] + 8, 3: A[0]}, hkv=0) == -7
         assert _rot(lib, {0: A[0] + 8, 2: A[1]}, hq=0) == -7
+
+
+def test_windows_past_32_bits_stay_windows():
+    from masked_grouped_query_b200.attention import _args
+    assert [_args(w, None, False)[1] for w in (None, 0, -1, 5, 2 ** 31, 2 ** 32, 2 ** 32 + 7, -2 ** 32 + 5)] \
+        == [0, 0, -1, 5, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, -2 ** 31]

@@ -282,3 +282,18 @@ def test_an_infinite_gradient_reaches_every_visible_key(path, d, lq, cap):
     assert torch.isfinite(dq[0, 0, :row]).all() and torch.isfinite(dq[0, 1:]).all()
     assert not torch.isfinite(dk[0, 0, :row + 1]).any()
     assert torch.isfinite(dk[0, 0, row + 1:]).all() and torch.isfinite(dk[0, 1]).all()
+
+
+# ---------------------------------------------------------------- arguments
+def test_windows_past_32_bits():
+    # A window longer than the keys hides none of them; it still is a window.
+    t, _ = make((1, 100, 100, 4, 2, 64, False, None, None, 1), seed=29)
+    q, k, v = t["q"], t["k"], t["v"]
+    o, lse = mgq.attention_lse(q, k, v, causal=True)
+    want = mgq.attention_backward(t["do"], q, k, v, o, lse, causal=True)
+    for window in (2 ** 31, 2 ** 32, 2 ** 32 + 7, 2 ** 40):
+        r = mgq.attention_lse(q, k, v, window=window)
+        assert torch.equal(r[0], o) and torch.equal(r[1], lse)
+        got = mgq.attention_backward(t["do"], q, k, v, o, lse, window=window)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert torch.equal(mgq.attention(q, k, v, window=window), mgq.attention(q, k, v, causal=True))
