@@ -53,11 +53,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         compiles = [subprocess.Popen([nvcc(), *flags, "-c", os.path.join(CSRC, u + ".cu"), "-o", o],
                                      stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
                     for u, o in zip(UNITS, objects)]
-        for u, proc in zip(UNITS, compiles):
-            out = proc.communicate()[0]
+        # Every compiler has ended before any failure is reported.
+        outputs = [proc.communicate()[0] for proc in compiles]
+        for u, proc, out in zip(UNITS, compiles, outputs):
             if proc.returncode != 0:
-                for other in compiles:
-                    other.communicate()
                 raise RuntimeError(f"nvcc failed on {u}.cu:\n{out}")
             if verbose:
                 sys.stderr.write(out)

@@ -28,3 +28,27 @@ def test_windows_past_32_bits_stay_windows():
     from masked_grouped_query_b200.attention import _args
     assert [_args(w, None, False)[1] for w in (None, 0, -1, 5, 2 ** 31, 2 ** 32, 2 ** 32 + 7, -2 ** 32 + 5)] \
         == [0, 0, -1, 5, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, -2 ** 31]
+
+
+def _fake_nvcc(tmp_path, monkeypatch, script):
+    """build.build() compiling into tmp_path with a shell script in place of nvcc."""
+    fake = tmp_path / "nvcc"
+    fake.write_text("#!/bin/sh\n" + script)
+    fake.chmod(0o755)
+    monkeypatch.setattr(build, "nvcc", lambda: str(fake))
+    monkeypatch.setattr(build, "PKG", str(tmp_path))
+    monkeypatch.setattr(build, "LIBRARY", str(tmp_path / "lib.so"))
+
+
+# Writes a line into the file named after -o.
+_WRITE = 'while [ "$1" != -o ]; do shift; done; echo made > "$2"\n'
+
+
+@pytest.mark.parametrize("unit", build.UNITS)
+def test_a_failed_compile_shows_the_compilers_message(tmp_path, monkeypatch, unit):
+    _fake_nvcc(tmp_path, monkeypatch,
+               f'case "$*" in *{unit}.cu*) echo "error: no such thing in {unit}"; exit 2;; esac\n'
+               "sleep 0.3\n" + _WRITE)
+    with pytest.raises(RuntimeError, match=f"no such thing in {unit}"):
+        build.build(force=True)
+    assert [p.name for p in tmp_path.iterdir()] == ["nvcc"]  # no objects left behind
