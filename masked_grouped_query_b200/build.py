@@ -12,6 +12,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -46,10 +47,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if (not force and os.path.exists(LIBRARY)
             and os.path.getmtime(LIBRARY) >= max(os.path.getmtime(d) for d in deps)):
         return LIBRARY
-    # Objects carry the process number: two builds at once do not meet.
-    objects = [os.path.join(PKG, f"{u}.{os.getpid()}.o") for u in UNITS]
     flags = [*NVCC_FLAGS, *(["-Xptxas=-v"] if verbose else []), f"-I{INCLUDE}"]
-    try:
+    # Objects and library are made in a folder of this build alone and the
+    # library is moved into place whole: two builds at once do not meet.
+    with tempfile.TemporaryDirectory(prefix="building-", dir=PKG) as tmp:
+        objects = [os.path.join(tmp, u + ".o") for u in UNITS]
         compiles = [subprocess.Popen([nvcc(), *flags, "-c", os.path.join(CSRC, u + ".cu"), "-o", o],
                                      stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
                     for u, o in zip(UNITS, objects)]
@@ -60,15 +62,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
                 raise RuntimeError(f"nvcc failed on {u}.cu:\n{out}")
             if verbose:
                 sys.stderr.write(out)
-        res = subprocess.run([nvcc(), *NVCC_FLAGS, "-shared", *objects, "-o", LIBRARY + ".tmp"],
+        made = os.path.join(tmp, os.path.basename(LIBRARY))
+        res = subprocess.run([nvcc(), *NVCC_FLAGS, "-shared", *objects, "-o", made],
                              capture_output=True, text=True)
         if res.returncode != 0:
             raise RuntimeError("nvcc failed to link:\n" + res.stdout + res.stderr)
-    finally:
-        for o in objects:
-            if os.path.exists(o):
-                os.remove(o)
-    os.replace(LIBRARY + ".tmp", LIBRARY)
+        os.replace(made, LIBRARY)
     return LIBRARY
 
 

@@ -1,4 +1,7 @@
 """Argument checks of the training operators and the build, without a device (CPU)."""
+import time
+from concurrent.futures import ThreadPoolExecutor
+
 import pytest
 import torch
 
@@ -52,3 +55,15 @@ def test_a_failed_compile_shows_the_compilers_message(tmp_path, monkeypatch, uni
     with pytest.raises(RuntimeError, match=f"no such thing in {unit}"):
         build.build(force=True)
     assert [p.name for p in tmp_path.iterdir()] == ["nvcc"]  # no objects left behind
+
+
+def test_two_builds_at_once_each_publish_a_whole_library(tmp_path, monkeypatch):
+    _fake_nvcc(tmp_path, monkeypatch, 'while [ "$1" != -o ]; do shift; done\n'
+               'echo first > "$2"; sleep 0.4; echo last >> "$2"\n')
+    with ThreadPoolExecutor(2) as pool:
+        first = pool.submit(build.build, force=True)
+        time.sleep(0.2)
+        second = pool.submit(build.build, force=True)
+        assert first.result() == second.result() == build.LIBRARY
+    assert (tmp_path / "lib.so").read_text() == "first\nlast\n"
+    assert sorted(p.name for p in tmp_path.iterdir()) == ["lib.so", "nvcc"]
