@@ -6,11 +6,17 @@ a visible key.  ``attention_backward`` takes it, the output and the output's
 gradient, recomputes the probabilities and returns the gradients of q, k and
 v.  Results over disjoint sets of keys merge by the same statistic:
 ``lse = logsumexp_s lse_s``, ``o = sum_s exp(lse_s - lse) o_s``.
+
+Neither these functions nor ``rotary`` record an autograd graph: a training
+step calls the backward functions itself, in an ``autograd.Function`` or under
+``torch.no_grad()``.  Called with tensors that require a gradient while
+gradients are recorded they warn, since ``loss.backward()`` stops there.
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
+import warnings
 
 import torch
 
@@ -36,6 +42,15 @@ def _on(stream):
     """Allocations for work on ``stream`` belong to that stream: their memory
     is then reused only after the work, whatever the current stream is."""
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _warn_no_graph(name, *tensors):
+    for t in tensors:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            warnings.warn(f"{name} records no autograd graph: gradients stop at its results, and its "
+                          "inputs require one (call it in an autograd.Function or under "
+                          "torch.no_grad())", stacklevel=3)
+            return
 
 
 def _check_qkv(q, k, v):
@@ -74,6 +89,7 @@ def attention_lse(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: 
                   stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """Masked GQA attention forward and its rows' log-sum-exp: ``(o, lse)``."""
     dims = _check_qkv(q, k, v)
+    _warn_no_graph("attention_lse", q, k, v)
     with _on(stream):
         if out is None:
             out = torch.empty_like(q)
@@ -107,6 +123,7 @@ def attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
     _check_rows("lse", lse, q)
     if dlse is not None:
         _check_rows("dlse", dlse, q)
+    _warn_no_graph("attention_backward", do, q, k, v, o, lse, dlse)
     c, w, s = _args(window, softcap, causal)
     lib = _lib.load()
     size = ctypes.c_size_t(0)

@@ -13,7 +13,7 @@ import ctypes
 import torch
 
 from . import _lib
-from .backward import _device, _on, _stream_of
+from .backward import _device, _on, _stream_of, _warn_no_graph
 
 IN_SEQ_MAJOR = 0x1
 OUT_SEQ_MAJOR = 0x2
@@ -70,6 +70,7 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, *, 
             or not positions.is_contiguous():
         raise ValueError(f"positions must be contiguous with shape {(len(sections), b, length)} on "
                          f"{device}, got {tuple(positions.shape)} on {positions.device}")
+    _warn_no_graph("rotary", q, k)
     if out_seq_major is None:
         out_seq_major = seq_major
     if out_dtype is None:

@@ -1,5 +1,6 @@
 """The training operators where their formulas are easy to get wrong (GPU)."""
 import math
+import warnings
 from decimal import Decimal, getcontext
 
 import pytest
@@ -297,3 +298,25 @@ def test_windows_past_32_bits():
         got = mgq.attention_backward(t["do"], q, k, v, o, lse, window=window)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert torch.equal(mgq.attention(q, k, v, window=window), mgq.attention(q, k, v, causal=True))
+
+
+def test_inputs_that_require_a_gradient_are_not_passed_over_in_silence():
+    t, _ = make((1, 20, 20, 2, 1, 64, False, None, None, 1), seed=31)
+    q, k, v, do = (t[n] for n in ("q", "k", "v", "do"))
+    o, lse = mgq.attention_lse(q, k, v)
+    pos = torch.zeros(1, 1, 20, dtype=torch.int32, device="cuda")
+    kr = k.expand(1, 2, 20, 64).contiguous()
+    calls = {"attention_lse": lambda: mgq.attention_lse(q, k, v),
+             "attention_backward": lambda: mgq.attention_backward(do, q, k, v, o, lse),
+             "rotary": lambda: mgq.rotary(q, kr, pos, sections=(32,))}
+    for name, call in calls.items():
+        with warnings.catch_warnings():
+            warnings.simplefilter("error")
+            want = call()
+            k.requires_grad_(), kr.requires_grad_()
+            with torch.no_grad():
+                call()
+        with pytest.warns(UserWarning, match=f"^{name} records no autograd graph"):
+            got = call()
+        k.requires_grad_(False), kr.requires_grad_(False)
+        assert all(torch.equal(a, b) and not a.requires_grad for a, b in zip(got, want))
