@@ -14,6 +14,22 @@ pytestmark = pytest.mark.gpu
 
 
 # ---------------------------------------------------------------- statistics with large softcaps
+ROW_MAX = [
+    # (batch, q_len, kv_len, hq, hkv, d, causal, window, softcap, spread of q)
+    (4, 700, 700, 16, 16, 64, True, None, 80.0, 1),        # not split; logits far below the cap
+    (4, 700, 700, 16, 16, 64, True, None, 80.0, 60),       # logits past the cap
+    (2, 640, 768, 32, 16, 128, False, None, 300.0, 30),    # not split, no mask
+    (2, 640, 768, 32, 16, 128, True, 200, 300.0, 200),
+    (1, 300, 500, 4, 2, 128, True, None, 80.0, 40),        # split
+    (1, 300, 500, 4, 2, 40, False, None, 300.0, 150),
+    (2, 200, 77, 4, 2, 72, True, None, 80.0, 20),          # rows without a visible key
+    (1, 400, 130, 4, 1, 64, True, 100, 300.0, 100),
+    (1, 40, 3000, 2, 1, 128, True, None, 80.0, 40),        # one row tile, paired splits
+    (1, 1, 2000, 32, 2, 64, True, 700, 300.0, 100),
+    (1, 333, 500, 4, 2, 256, True, 200, 300.0, 100),       # wide heads
+]
+
+
 def check_forward_and_gradients(case, kw, t, path):
     f = ref.forward(t["q"], t["k"], t["v"], **kw)
     o, lse = forced(path, lambda: mgq.attention_lse(t["q"], t["k"], t["v"], **kw))
@@ -29,6 +45,26 @@ def check_forward_and_gradients(case, kw, t, path):
     for n, g, w, b in zip(("dq", "dk", "dv"), got, want, bound):
         ref.assert_within(n, g, w, b)
     assert mgq.status() & 0x1f == 0
+
+
+@pytest.mark.parametrize("case,path", [(c, p) for c in ROW_MAX for p in ((0, 1, 2) if c[5] <= 128 else (0,))],
+                         ids=str)
+def test_row_max_softcap(case, path):
+    # Caps above about 63.8 keep a running maximum.
+    t, kw = make(case, seed=20)
+    check_forward_and_gradients(case, kw, t, path)
+
+
+@pytest.mark.parametrize("cap", [30.0, 50.0])
+@pytest.mark.parametrize("case", [c for c in ROW_MAX if c[5] <= 128], ids=str)
+def test_row_max_softcap_by_override(case, cap):
+    t, kw = make(case, seed=21)
+    kw["softcap"] = cap
+    mgq.set_override("softcap_two_pass", 1)
+    try:
+        check_forward_and_gradients(case, kw, t, 2)
+    finally:
+        mgq.set_override("softcap_two_pass", 0)
 
 
 # ---------------------------------------------------------------- rotary
