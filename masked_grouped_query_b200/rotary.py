@@ -60,7 +60,10 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, *, 
             bk, hkv, lk, dk = k.shape
         if bk != b or lk != length or dk != d:
             raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}")
-    sections = [_section(s) for s in sections]
+    given = list(sections)
+    sections = [int(s) for s in given]
+    if sections != given or sections and (max(sections) > 2 ** 31 - 1 or min(sections) < -2 ** 31):
+        raise ValueError(f"sections must be whole numbers of 32 bits, got {given}")
     if not isinstance(positions, torch.Tensor):
         raise TypeError("positions must be a torch.Tensor")
     if positions.dtype not in (torch.int32, torch.int64):
@@ -105,13 +108,6 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, *, 
             _stream_of(stream, device))
     _lib.check(rc, "gqa_attn_rotary")
     return q_out, k_out
-
-
-def _section(s):
-    n = int(s)
-    if n != s or not -2 ** 31 <= n < 2 ** 31:  # a C int would take another value
-        raise ValueError(f"sections must be whole numbers of 32 bits, got {s}")
-    return n
 
 
 def _check(name, t, q):
