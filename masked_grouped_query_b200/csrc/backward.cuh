@@ -29,7 +29,7 @@ namespace gqa {
 
 constexpr float kLog2e32 = 1.4426950408889634f;
 
-// Rows as the backward kernels see them: `seqs` runs of `run` consecutive
+// Rows as the backward kernels see them: `runs` runs of `run` consecutive
 // rows (row r of a run is query r % q_len), cut into tiles of 128 that do not
 // cross runs.  A run is a q head when a mask makes most tiles of a head
 // skippable (q_len >= 256), else the whole group of a kv head, which wastes
@@ -340,6 +340,14 @@ __global__ void __launch_bounds__(kBmThreads, 1) bwd_mma_kernel(const BwdParams 
 #pragma unroll
   for (int i = 0; i < (kDQ ? 1 : KS); ++i) acc2[i][0] = acc2[i][1] = acc2[i][2] = acc2[i][3] = 0.f;
 
+  // What thread t (< 192) brings of the query rows' 192 numbers.  dQ's CTAs read
+  // past L1 (see the head of backward_sm100.cuh), once: the rows are their own.
+  auto row_stat = [&](long long run, int q_row0) {
+    const int w = threadIdx.x >> 6, r = threadIdx.x & 63;
+    const float* at = p.stats + (run * s.tiles + (q_row0 >> 7)) * 256 + w * 128 + (q_row0 & 127) + r;
+    return w == 2 ? __int_as_float(s.kv_len - s.q_len + (q_row0 + r) % s.q_len) : kDQ ? __ldcg(at) : *at;
+  };
+  if (kDQ && threadIdx.x < 192) st2[threadIdx.x] = st2[192 + threadIdx.x] = row_stat(run0, own_row0);
   // Tile `it` of the walk into its buffer.
   auto fetch = [&](int it) {
     const long long run = run0 + (kDQ ? 0 : it / count);
@@ -349,12 +357,7 @@ __global__ void __launch_bounds__(kBmThreads, 1) bwd_mma_kernel(const BwdParams 
     const long long off = (kDQ ? unit * s.kv_len + row0 : run * s.run + row0) * (long long)D;
     bwd_load_tile<KS>(s1, (kDQ ? p.k : p.q) + off, D, n);
     bwd_load_tile<KS>(s1 + C::kTileElems, (kDQ ? p.v : p.dout) + off, D, n);
-    if (threadIdx.x < 192) {
-      const int w = threadIdx.x >> 6, r = threadIdx.x & 63, q_row0 = kDQ ? own_row0 : row0;
-      st2[((it - begin) & 1) * 192 + threadIdx.x] =
-          w < 2 ? p.stats[(run * s.tiles + (q_row0 >> 7)) * 256 + w * 128 + (q_row0 & 127) + r]
-                : __int_as_float(s.kv_len - s.q_len + (q_row0 + r) % s.q_len);
-    }
+    if (!kDQ && threadIdx.x < 192) st2[((it - begin) & 1) * 192 + threadIdx.x] = row_stat(run, row0);
     cp_async_commit();
   };
   if (begin < end) {

@@ -37,8 +37,10 @@
 // everywhere, so on small problems the two run side by side, and on large ones
 // dQ's CTAs take each SM as it becomes free.  The chain: the dK/dV kernel
 // waits for the statistics, then lets dQ's CTAs start (the statistics are
-// therefore complete for them too); dQ's last CTA waits for the dK/dV kernel
-// before it ends, so that whatever follows in the stream finds both done.
+// therefore complete for them too; they read them past L1, since without a
+// wait of their own nothing promises that L1 holds no older ones); dQ's last
+// CTA waits for the dK/dV kernel before it ends, so that whatever follows in
+// the stream finds both done.
 //
 // kFine: P and dS go to the tensor core as two bf16 terms each, the rounded
 // value and the rounded rest, so that the gradients' only rounding that counts
@@ -884,7 +886,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
     Item it = item_at(i);
     for (int kk = 1; i < items && ok; ++kk) {
       const float* st = p.stats + ((long long)it.run * s.tiles + it.tile) * 256;
-      const float nlse = st[r], delta = st[128 + r];
+      const float nlse = __ldcg(st + r), delta = __ldcg(st + 128 + r);  // from L2 (see the head)
       int lo = 0, hi = -1;
       if (r < it.nr) {
         const int qpos = s.kv_len - s.q_len + (it.r0 + r) % s.q_len;

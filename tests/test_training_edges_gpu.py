@@ -321,6 +321,31 @@ def test_an_infinite_gradient_reaches_every_visible_key(path, d, lq, cap):
     assert torch.isfinite(dk[0, 0, row + 1:]).all() and torch.isfinite(dk[0, 1]).all()
 
 
+# ---------------------------------------------------------------- the chain of kernels
+@pytest.mark.parametrize("case", [(1, 128, 128, 4, 1, 128, True, None, None, 1),
+                                  (2, 700, 900, 8, 2, 64, True, None, None, 1),
+                                  (1, 300, 450, 4, 2, 256, True, 200, None, 1)], ids=str)
+def test_every_replay_reads_its_own_statistics(case):
+    # The dQ kernel does not wait for the statistics itself: one scratch, inputs in turn.
+    sets = []
+    for seed in (32, 33):
+        t, kw = make(case, seed=seed)
+        o, lse = mgq.attention_lse(t["q"], t["k"], t["v"], **kw)
+        args = [t["do"], t["q"], t["k"], t["v"], o, lse]
+        sets.append((args, mgq.attention_backward(*args, **kw)))
+    now = [torch.empty_like(x) for x in sets[0][0]]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = mgq.attention_backward(*now, **kw)
+    for turn in range(100):
+        args, want = sets[turn & 1]
+        for a, b in zip(now, args):
+            a.copy_(b)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), turn
+
+
 # ---------------------------------------------------------------- arguments
 def test_windows_past_32_bits():
     # A window longer than the keys hides none of them; it still is a window.
