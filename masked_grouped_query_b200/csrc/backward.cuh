@@ -53,6 +53,7 @@ struct BwdParams {
   float logit_scale;   // log2(e) / sqrt(D)
   float cap_in;        // 1 / (sqrt(D) * cap)
   float cap_out;       // cap * log2(e)
+  float poly_most;     // largest |x * cap_in| for the degree-7 polynomial (tcgen05)
   // Parts of a tile's walk; with more than one, their fp32 partials: part i is
   // [columns rounded up to 16, by 4][tile rows][4].
   int kv_splits, q_splits;

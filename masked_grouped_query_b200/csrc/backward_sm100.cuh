@@ -101,7 +101,7 @@ __device__ __forceinline__ void bwd_probs(const BwdParams& p, const uint32_t (&s
 #pragma unroll
     for (int c = 0; c < 32; c += 2)
       am = fmax3(am, fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
-    const bool small = __all_sync(0xffffffffu, am * p.cap_in <= 0.5f);
+    const bool small = __all_sync(0xffffffffu, am * p.cap_in <= p.poly_most);
     const f2 co = f2_pack(p.cap_out, p.cap_out), one = f2_pack(1.f, 1.f);
     if (small) {
       // tanh(x cap_in) as x Q(x^2), cap_in folded into the coefficients.

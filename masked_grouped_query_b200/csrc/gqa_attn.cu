@@ -682,6 +682,9 @@ int launch_prefill_k(const Problem& pr, const Plan& pl, DeviceInfo& dev, int csi
   p.logit_scale = kLog2e * rs;
   p.cap_in = kCap ? gqa_host::softcap_in(rs, pr.softcap) : 0.f;
   p.cap_out = kCap ? pr.softcap * kLog2e : 0.f;
+  constexpr float k13[7] = {kTanh13C1, kTanh13C3,  kTanh13C5, kTanh13C7,
+                            kTanh13C9, kTanh13C11, kTanh13C13};
+  p.poly_most = kLse && kCap ? gqa_host::softcap_fold_most(k13, p.cap_in, p.cap_out, 1.f) : 0.f;
   // Fixed exponent base (softcap code 3, see PrefillParams and cap_degree).
   p.cap_fixed = kCapDeg == 3 ? 1 : 0;
   p.cap_base = kCapDeg == 3 ? p.cap_out - cap_base_offset(p.cap_out) : 0.f;

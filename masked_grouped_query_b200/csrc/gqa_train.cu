@@ -310,11 +310,10 @@ int gqa_attn_bwd(const void* dout, const void* q, const void* k, const void* v, 
   p.softcap = softcap > 0.f;
   p.scale = 1.0f / std::sqrt((float)head_dim);
   p.cap_in = p.softcap ? gqa_host::softcap_in(p.scale, softcap) : 0.f;
-  // Narrow heads take the mma.sync kernels too (uncut) when asked by
-  // force_path 1, and with softcaps for which the tcgen05 kernels cannot fold
-  // the powers of cap_in into their polynomial.
-  const bool folds = !p.softcap || (p.cap_in >= kFoldMinCapIn && p.cap_in <= kFoldMaxCapIn);
-  const bool narrow_mma = head_dim <= 128 && (gqa_host::forced_path() == 1 || !folds);
+  constexpr float k7[4] = {kTanhC1, kTanhC3, kTanhC5, kTanhC7};
+  p.poly_most = p.softcap ? gqa_host::softcap_fold_most(k7, p.cap_in, 1.f, 0.5f) : 0.f;
+  // (force_path 1 takes the mma.sync kernels for narrow heads too, uncut.)
+  const bool narrow_mma = head_dim <= 128 && gqa_host::forced_path() == 1;
   const BwdPlan pl = bwd_plan(s, !narrow_mma);
   const size_t need = work ? pl.bytes : 0;
   if (need && !scratch) return GQA_ATTN_ERR_NULL_POINTER;

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cfloat>
+#include <cmath>
 
 #include <algorithm>
 
@@ -34,8 +35,24 @@ int detail(int code, const char* fmt, ...);
 // changes a logit up to 1e26 in fp32 (by (x / cap)^2 / 3 of itself), and with
 // this one the scales derived from it stay normal numbers.
 constexpr float kSoftcapMost = 1e30f;
-// 1 / (sqrt(head_dim) * softcap), finite for every softcap.
-inline float softcap_in(float scale, float softcap) { return std::min(scale / softcap, FLT_MAX); }
+// 1 / (sqrt(head_dim) * softcap), finite (and so with log2(e) etc.) for every softcap.
+inline float softcap_in(float scale, float softcap) { return std::min(scale / softcap, 1e37f); }
+
+// The kernels evaluate scale * tanh(x * cap_in) as x Q(x^2), with scale and
+// cap_in's powers folded into the coefficients k of tanh's odd polynomial on
+// [0, most] (one product per pair of scores less than scaling x first).  The
+// largest |x * cap_in| for which that is good to 2e-8: `most`, less where a term
+// underflows, so that what is lost of it stays below; none (-1) where powers
+// could overflow, for softcaps below 1e-3.  Past it they take an exponential.
+template <int N>
+float softcap_fold_most(const float (&k)[N], float cap_in, float scale, float most) {
+  if (cap_in > 1e3f) return -1.f;
+  double f = (double)scale * cap_in;
+  for (int i = 0; i < N; ++i, f *= (double)cap_in * cap_in)
+    if (std::fabs(f * k[i]) < FLT_MIN)
+      most = std::min(most, (float)std::pow(2e-8 / std::fabs(k[i]), 1.0 / (2 * i + 1)));
+  return most;
+}
 
 bool overlaps(const void* a, size_t na, const void* b, size_t nb);
 

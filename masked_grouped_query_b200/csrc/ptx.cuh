@@ -447,12 +447,6 @@ constexpr float kTanh13C7 = -0.05349045619368553f;
 constexpr float kTanh13C9 = 0.0202915258705616f;
 constexpr float kTanh13C11 = -0.006167485378682613f;
 constexpr float kTanh13C13 = 0.0010202169651165605f;
-// Folding cap_in's powers into a polynomial's coefficients saves one product
-// per pair of scores and works between these: past the first (softcaps below
-// 1e-3) the 13th power overflows, below the second (softcaps past 10^4) the 7th,
-// of the backward pass, is no normal number.
-constexpr float kFoldMaxCapIn = 1e3f;
-constexpr float kFoldMinCapIn = 1e-5f;
 __device__ __forceinline__ float tanh_poly13(float y) {
   const float y2 = y * y;
   float q = fmaf(kTanh13C13, y2, kTanh13C11);
