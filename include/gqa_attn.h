@@ -118,10 +118,10 @@ int gqa_attn_fwd(const void* q, const void* k, const void* v, void* o, int batch
 /*
  * gqa_attn_fwd_lse -- gqa_attn_fwd that also returns every row's log-sum-exp,
  * lse[b][h][i] = ln(sum over visible keys of e^x) in fp32 (-inf for a row
- * without a visible key; o is zero there).  A row with a NaN logit, or with an
- * infinite one and no softcap, gets NaN in both: it is not taken for empty.
- * The backward pass reads lse, and it merges results over disjoint sets of
- * keys: o = sum_s e^(lse_s - lse) o_s.
+ * without a visible key, or with -inf logits only; o is zero there).  A row
+ * with a NaN logit, or with one of +inf and no softcap, gets NaN in both: it is
+ * not taken for empty.  The backward pass reads lse, and it merges results over
+ * disjoint sets of keys: o = sum_s e^(lse_s - lse) o_s.
  *
  * lse: device pointer, [batch][num_q_heads][q_len] fp32, 16-byte aligned,
  * overlapping no other argument; the caller owns it.  Everything else,

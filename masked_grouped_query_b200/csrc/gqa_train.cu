@@ -109,10 +109,12 @@ int bwd_splits(long long items, long long steps, int tile) {
 // Problems of at most this many steps (one per SM) take P and dS in two bf16
 // terms.  Their gradients' error, in the 2-norm, then is the outputs' rounding
 // alone, 1.7e-3; with one term it is 2.4e-3, and where few products make a
-// gradient up to twice the rounding.  Measured, microseconds with one and two
-// terms (captured calls): 23 and 27 (1, 128, 128, 4:1, 128), 16 and 20 (1, 512,
-// 512, 2:2, 128), less than the host takes to launch either; but 21 and 27 for
-// 512 steps (1, 1024, 1024, 8:8, 64), 1519 and 2159 for the largest case.
+// gradient up to twice the rounding.  So the same rows may give gradients that
+// differ by that rounding in a larger batch.  Measured, microseconds with one
+// and two terms (captured calls): 23 and 27 (1, 128, 128, 4:1, 128), 16 and 20
+// (1, 512, 512, 2:2, 128), where an uncaptured call takes 28 for its launches
+// anyhow; but 21 and 27 for 512 steps (1, 1024, 1024, 8:8, 64), 1519 and 2159
+// for the largest case.
 constexpr long long kBwFineSteps = 148;
 
 BwdPlan bwd_plan(const BwdShape& s, bool may_split) {
