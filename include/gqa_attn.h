@@ -120,8 +120,10 @@ int gqa_attn_fwd(const void* q, const void* k, const void* v, void* o, int batch
  * lse[b][h][i] = ln(sum over visible keys of e^x) in fp32 (-inf for a row
  * without a visible key, or with -inf logits only; o is zero there).  A row
  * with a NaN logit, or with one of +inf and no softcap, gets NaN in both: it is
- * not taken for empty.  The backward pass reads lse, and it merges results over
- * disjoint sets of keys: o = sum_s e^(lse_s - lse) o_s.
+ * not taken for empty.  A NaN or an infinity in k at a key that a row does not
+ * see leaves the row alone; one in v may reach its o (0 * NaN), not its lse.
+ * The backward pass reads lse, and it merges results over disjoint sets of
+ * keys: o = sum_s e^(lse_s - lse) o_s.
  *
  * lse: device pointer, [batch][num_q_heads][q_len] fp32, 16-byte aligned,
  * overlapping no other argument; the caller owns it.  Everything else,
@@ -152,9 +154,11 @@ int gqa_attn_fwd_lse(const void* q, const void* k, const void* v, void* o, float
  * tensor cores (small problems take two bf16 terms of each), sums are fp32,
  * each gradient is rounded once.  A row without
  * a visible key (lse = -inf) gives and gets no gradient; a key that no query
- * sees gets zeros.  Masked scores count as exact zeros, but a NaN or an
- * infinity in k, v, q or dout still reaches every gradient whose products
- * multiply it, as in a dense matrix product.
+ * sees gets zeros.  A NaN or an infinity in k, v, q or dout reaches the
+ * gradients of every pair that the mask leaves visible, P = 0 included, as in
+ * a dense matrix product.  P and ds of hidden pairs are exact zeros, but a
+ * tile's products multiply them too: a NaN or an infinity in a row that is
+ * hidden from some of a tile's rows may reach those (0 * NaN).
  *
  * scratch: caller-owned device memory, 16-byte aligned, of at least the bytes
  * that gqa_attn_bwd_scratch reports for these sizes; its contents need not

@@ -305,6 +305,21 @@ def test_a_row_of_minus_infinities_below_the_cap(case):
     assert ((o[0, 0, row].double() - v.mean(0)).abs() <= 2 * ref.U16 * v.abs().mean(0) + 1e-30).all()
 
 
+@pytest.mark.parametrize("value", ["nan", "inf", "-inf"])
+@pytest.mark.parametrize("case", [c for c in NAN_ROWS if c[6]], ids=str)
+def test_keys_that_are_not_numbers_leave_the_rows_before_them_alone(case, value):
+    case, path = dims(case)
+    t, kw = make(case, seed=34)
+    f = ref.forward(t["q"], t["k"], t["v"], **kw)
+    row = case[1] // 2                             # the first row that sees such a key
+    t["k"][:, :, case[2] - case[1] + row:, 1::5] = float(value)
+    o, lse = forced(path, lambda: mgq.attention_lse(t["q"], t["k"], t["v"], **kw))
+    ref.assert_within("o", o[:, :, :row], f["o"][:, :, :row], ref.o_bound(f)[:, :, :row])
+    ref.assert_within("lse", lse[:, :, :row], f["lse"][:, :, :row], ref.lse_bound(f)[:, :, :row])
+    if value == "nan" and kw["window"] is None:  # every later row sees one
+        assert torch.isnan(lse[:, :, row:]).all()
+
+
 @pytest.mark.parametrize("path,d,lq", [(0, 64, 256), (0, 128, 256), (0, 128, 200), (1, 128, 256), (0, 256, 256)])
 @pytest.mark.parametrize("cap", [None, 50.0])
 def test_an_infinite_gradient_reaches_every_visible_key(path, d, lq, cap):
